@@ -188,6 +188,118 @@ int pivot_decode_index_paged(const void* q, const void* kpages, const int32_t* b
                              size_t workspace_bytes, void* stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * The serving step around the indexer, over a paged cache.
+ *
+ * A layer that keeps its keys in pages (pivot_decode_index_paged) norms and
+ * rotates its queries and keys, writes the new keys and values into the pages,
+ * and attends: densely over the cache, or over the index rows.  The calls below
+ * share these conventions:
+ *  - New tokens are numbered 0 .. T-1, sequence after sequence.  With cu (device
+ *    int32 [B+1], non-decreasing) sequence b has tokens cu[b] .. cu[b+1]-1;
+ *    without it every sequence has g (T = B * g).  Tokens behind cu[B] belong to
+ *    no sequence: their output rows are left as they were.
+ *  - seqlens[b] (device int32 [B]) is the rows that sequence b holds with its
+ *    n_b new ones: new token i sits at row (position) seqlens[b] - n_b + i.
+ *  - kpages, vpages: bf16 [num_pages][page_size][heads][d], page_size a power of
+ *    two; block_table: int32 [B][max_pages] (device).
+ *  - The device arrays are checked where they are used: a sequence whose lengths
+ *    contradict each other or exceed max_pages * page_size (or max_seqlen, where
+ *    given) is skipped, and so is a row whose page is not in [0, num_pages); both
+ *    are reported by pivot_sync_status() as PIVOT_ERR_INVALID_ARG.
+ *  - d is 64 or 128.  fp32 arithmetic; each result is rounded once.
+ */
+
+/* Type of a call's inputs, and how a rotation pairs the first rot_dim channels:
+ * (i, i + rot_dim/2), or (2i, 2i+1). */
+typedef enum { PIVOT_BF16 = 0, PIVOT_FP16 = 1, PIVOT_FP32 = 2 } pivot_dtype_t;
+typedef enum { PIVOT_ROPE_HALF = 0, PIVOT_ROPE_INTERLEAVED = 1 } pivot_rope_layout_t;
+
+/* Head rows [T][heads][d] of new tokens, strides in elements (each row must
+ * start on a 16-byte boundary; channels are adjacent), with the weight [d] of
+ * the norm of each head, in the same type (NULL: no norm). */
+typedef struct {
+  const void* data;
+  const void* weight;
+  long long token_stride;
+  long long head_stride;
+  int heads;
+} pivot_heads_t;
+
+/* The rotation, and the norm's eps.  freqs: fp64 [rot_dim/2] (device), radians a
+ * position of each pair, whatever scaling made them; NULL: no rotation.
+ * amplitude multiplies the cosines and sines (1 without scaling).  rot_dim is a
+ * multiple of 16, at most d; channels behind it are passed on. */
+typedef struct {
+  const double* freqs;
+  double amplitude;
+  double eps;
+  int rot_dim;
+  int layout;
+} pivot_rope_t;
+
+/*
+ * Norm and rotation of query and key heads in one pass: for each head row x of a
+ * token at position pos, x_c <- x_c (mean x^2 + eps)^-1/2 w_c where a weight is
+ * given, then each pair (a, b) of the first rot_dim channels becomes
+ * amplitude * (a cos t - b sin t, b cos t + a sin t), t = pos * freqs[i].
+ * positions: int32 [T] (device).  q or k may be NULL.  The angle is reduced in
+ * fp64, so any int32 position is exact to fp32.
+ * out_q, out_k: bf16 [T][heads][d], contiguous; they may be the inputs
+ * themselves (bf16, contiguous), and must not overlap them otherwise.
+ */
+int pivot_qk_rope(const pivot_heads_t* q, const pivot_heads_t* k, int dtype, const int32_t* positions,
+                  const pivot_rope_t* rope, int T, int d, void* out_q, void* out_k, void* stream);
+
+/*
+ * Writes the new keys (normed and rotated as above, at their rows' positions)
+ * and values (NULL: a cache of keys alone) into their pages, and, where q is
+ * given, norms and rotates the tokens' queries into out_q (bf16 [T][heads][d])
+ * in the same launch.  The new tokens' rows must be in pages of their own: two
+ * sequences that write the same row race.  A skipped sequence's rows and queries
+ * are left as they were.
+ */
+int pivot_paged_append(const pivot_heads_t* k, const pivot_heads_t* v, const pivot_heads_t* q, int dtype,
+                       const pivot_rope_t* rope, const int32_t* block_table, const int32_t* seqlens,
+                       const int32_t* cu_new, int T, int B, int d, int g, int num_pages, int page_size, int max_pages,
+                       void* kpages, void* vpages, void* out_q, void* stream);
+
+/* scale: of the scores (> 0).  include_self: a query at position pos sees the
+ * keys j <= pos; 0: j < pos, the keys that the indexer selects from. */
+typedef struct {
+  double scale;
+  int include_self;
+} pivot_attend_t;
+
+/*
+ * Dense causal attention of the new tokens over the paged cache (their own keys
+ * and values already appended): for query head h and the keys of head
+ * h / (Hq / Hk),
+ *     out = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
+ * over the keys that the query sees; a query that sees none, and every query of
+ * a skipped sequence, gets zeros and lse = -inf.
+ * q, out: bf16 [T][Hq][d]; out_lse: float32 [T][Hq] or NULL.  options NULL:
+ * scale d^-1/2, include_self.  max_seqlen: an upper bound on seqlens[b]; a
+ * longer sequence is skipped.  Keys and values that a query does not see may
+ * hold anything.  workspace as in the _ws variants; the size may be 0.
+ */
+size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int max_seqlen);
+int pivot_paged_attention(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
+                          const int32_t* seqlens, const int32_t* cu_q, const pivot_attend_t* options, int T, int B,
+                          int Hq, int Hk, int d, int g, int num_pages, int page_size, int max_pages, int max_seqlen,
+                          void* out, float* out_lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pivot_sparse_attention over a paged cache: q bf16 [B][g][H][d], idx int32
+ * [B][g][H][top_k] (the rows of pivot_decode_index_paged), out float32
+ * [B][g][H][d].  An index at or beyond seqlens[b], or whose page is not in the
+ * cache, is left out and reported.
+ */
+int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
+                                 const int32_t* seqlens, const int32_t* idx, int B, int H, int d, int g, int num_pages,
+                                 int page_size, int max_pages, int top_k, float* out, void* stream);
+
+/*
  * As the _ws variants, with two more nullable outputs that expose the
  * method's intermediate results ("How It Works": the proxy of each group and
  * its candidate set C = top-Kc of the proxy scores):
@@ -235,7 +347,8 @@ int pivot_decode_index_noalloc(const void* q, const void* kcache, const int32_t*
  * Synchronises `stream`, then reads and clears this device's kernel status
  * word.  Returns PIVOT_OK, PIVOT_ERR_TIMEOUT (a bounded wait inside a kernel
  * gave up; that call's outputs are not valid), PIVOT_ERR_INVALID_ARG (a decode
- * sequence exceeded max_seqlen) or PIVOT_ERR_CUDA (a CUDA error, or status bit
+ * sequence exceeded max_seqlen, or status bit 16: a page outside the cache or an
+ * index outside its sequence) or PIVOT_ERR_CUDA (a CUDA error, or status bit
  * 8: a refine selection exceeded its round limit, which finite scores never
  * do; that call's outputs are not valid).  *flags (nullable) receives the raw
  * status bits; bit 4 means some rows took the exact fallback path (results

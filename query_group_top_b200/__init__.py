@@ -9,23 +9,35 @@ library or an sm_100 device every call raises.
     idx = pivot_index(q, k, 16, 2048, 4096, REFINE, proxy="bf16")      # the bf16-proxy variant
     idx = dense_index(q, k, top_k=2048)
     idx = pivot_decode_index(q, kcache, cu_seqlens, g=2, top_k=2048, Kc=4096, max_seqlen=...)
+
+The serving step around the indexer, over a paged cache:
+
+    freqs, amp = rope_frequencies(128, scaling="yarn", factor=8.0, original_length=16384)
+    q, k = qk_rope(q, k, positions, freqs, amplitude=amp, q_weight=wq, k_weight=wk)     # prefill, no cache
+    q = paged_append(k, v, kpages, vpages, table, seqlens, freqs=freqs, q=q)            # a step's keys and values
+    idx = pivot_decode_index_paged(q, kpages, table, seqlens, g=2, top_k=2048, Kc=4096, max_seqlen=...)
+    o = sparse_attention_paged(q, kpages, vpages, table, seqlens, idx)                  # over the index rows
+    o = paged_attention(q, kpages, vpages, table, seqlens, max_seqlen)                  # or over every key
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
 
 __all__ = ["REFINE", "REUSE", "PROXY_BF16", "PER_MEMBER_SCAN", "PivotError", "pivot_index", "dense_index", "pivot_decode_index",
            "pivot_decode_index_paged", "sparse_attention",
+           "rope_frequencies", "qk_rope", "paged_append", "paged_attention", "sparse_attention_paged",
            "sync_status", "trace_enable", "trace_collect", "library_path", "load_library", "EXPORTED",
            "head_range"]
 
 REFINE, REUSE = 0, 1
 PROXY_BF16 = 0x100          # option bit of `mode`: scan with the bf16-rounded mean
 PER_MEMBER_SCAN = 0x200     # option bit of REFINE: each member's own-prefix candidate set
-FLAG_TIMEOUT, FLAG_BADLEN, FLAG_FALLBACK, FLAG_NOCONVERGE = 1, 2, 4, 8
+FLAG_TIMEOUT, FLAG_BADLEN, FLAG_FALLBACK, FLAG_NOCONVERGE, FLAG_BADPAGE = 1, 2, 4, 8, 16
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libpivot.so")
@@ -38,12 +50,27 @@ EXPORTED = (
     "pivot_decode_workspace_size", "pivot_decode_index_ws", "pivot_sync_status", "pivot_last_error",
     "pivot_trace_enable", "pivot_trace_collect", "pivot_decode_index_noalloc",
     "pivot_index_ex", "pivot_decode_index_ex", "pivot_set_wait_limit", "pivot_decode_index_paged",
-    "pivot_sparse_attention",
+    "pivot_sparse_attention", "pivot_qk_rope", "pivot_paged_append", "pivot_paged_attention_workspace_size",
+    "pivot_paged_attention", "pivot_sparse_attention_paged",
 )
 
 
 class PivotError(RuntimeError):
     pass
+
+
+class _Heads(ctypes.Structure):      # pivot_heads_t
+    _fields_ = [("data", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("heads", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):       # pivot_rope_t
+    _fields_ = [("freqs", ctypes.c_void_p), ("amplitude", ctypes.c_double), ("eps", ctypes.c_double),
+                ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class _Attend(ctypes.Structure):     # pivot_attend_t
+    _fields_ = [("scale", ctypes.c_double), ("include_self", ctypes.c_int)]
 
 
 def library_path() -> str:
@@ -79,6 +106,11 @@ def load_library():
         "pivot_decode_index_paged": ([P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P, P, Z, P], I),
         "pivot_sparse_attention": ([P, P, P, P, P, I, I, I, I, I, P, P], I),
         "pivot_set_wait_limit": ([ctypes.c_ulonglong], I),
+        "pivot_qk_rope": ([P, P, I, P, P, I, I, P, P, P], I),
+        "pivot_paged_append": ([P, P, P, I, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P], I),
+        "pivot_paged_attention_workspace_size": ([I, I, I, I, I, I], Z),
+        "pivot_paged_attention": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P, P, Z, P], I),
+        "pivot_sparse_attention_paged": ([P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -309,6 +341,315 @@ def sparse_attention(q, k, v, idx, cu_seqlens=None, g=1, out=None, stream=None):
     rc = lib.pivot_sparse_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), idx.data_ptr(), cu_ptr, R, H, d, g,
                                     top_k, out.data_ptr(), _stream_ptr(stream))
     _err(lib, rc)
+    return out
+
+
+# ------------------------------------------------------------------ the serving step over a paged cache
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_NOTHING = contextlib.nullcontext()
+
+
+def _where(device, stream, tensors):
+    """(raw stream, context) of a call on `device`: the given stream, or the device's current one, with the device
+    made current.  What the call allocates belongs to that stream; inputs that were made on another one are marked
+    as used by it, so that freeing them does not hand their memory out under the call."""
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+        ctx = _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return s.cuda_stream, ctx
+    if stream.device != device:
+        raise PivotError(f"the stream is of {stream.device}, the tensors are on {device}")
+    if stream != torch.cuda.current_stream(device):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _on_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise PivotError(f"{name} must be on {device} (is on {t.device})")
+
+
+def _tokens(name, x, g_shape=None):
+    """(leading shape, heads, d) of new tokens' rows x: [T, H, d], or [B, g, H, d]."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise PivotError(f"{name} must be a CUDA tensor")
+    if x.dim() not in (3, 4):
+        raise PivotError(f"{name} must be [T, heads, d] or [B, g, heads, d]")
+    return tuple(x.shape[:-2]), x.shape[-2], x.shape[-1]
+
+
+def _heads(name, x, weight, lead, d, dtype):
+    """pivot_heads_t of x [*lead, heads, d], which may be a strided view (a slice of a fused projection)."""
+    if x is None:
+        if weight is not None:
+            raise PivotError(f"a norm weight without {name}")
+        return None
+    got, H, dx = _tokens(name, x)
+    if got != lead or dx != d:
+        raise PivotError(f"{name} must be {[*lead]} tokens of heads of {d} channels (got {[*x.shape]})")
+    if x.dtype != dtype or dtype not in _DTYPES:
+        raise PivotError(f"{name} must be bfloat16, float16 or float32, and the call's tensors of one type (got {x.dtype})")
+    st = x.stride()
+    if st[-1] != 1:
+        raise PivotError(f"{name}'s channels must be adjacent")
+    ts = st[-3]
+    if x.dim() == 4:
+        if x.shape[1] == 1:
+            ts = st[0]
+        elif x.shape[0] > 1 and st[0] != x.shape[1] * st[1]:
+            raise PivotError(f"{name}'s tokens must be evenly spaced (strides {st})")
+    if x.numel() == d * H:
+        ts = 0
+    hs = st[-2] if H > 1 else 0
+    step = 16 // x.element_size()
+    if x.data_ptr() % 16 or ts % step or hs % step or H < 1:
+        raise PivotError(f"{name}'s rows must start on 16-byte boundaries")
+    if weight is not None:
+        if weight.dtype != dtype or tuple(weight.shape) != (d,) or not weight.is_contiguous() or weight.device != x.device \
+                or weight.data_ptr() % 16:
+            raise PivotError(f"{name}_weight must be a contiguous, 16-byte aligned {dtype} tensor of {d} channels on {x.device}")
+    return _Heads(x.data_ptr(), _ptr(weight), ts, hs, H)
+
+
+def _rope(freqs, layout, amplitude, eps, d, device):
+    if layout not in _LAYOUTS:
+        raise PivotError('layout must be "half" or "interleaved"')
+    if not (eps >= 0.0 and math.isfinite(eps) and math.isfinite(amplitude)):
+        raise PivotError("eps must be >= 0, and eps and amplitude finite")
+    if freqs is None:
+        return _Rope(None, 1.0, eps, 0, 0)
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous() or freqs.device != device:
+        raise PivotError(f"freqs must be a contiguous float64 vector of rot_dim / 2 frequencies on {device}")
+    rot = 2 * freqs.numel()
+    if rot < 16 or rot > d or rot % 16:
+        raise PivotError(f"rot_dim must be a multiple of 16 in [16, d] (got {rot})")
+    return _Rope(freqs.data_ptr(), amplitude, eps, rot, _LAYOUTS[layout])
+
+
+def _int32(name, t, device, shape):
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous()
+            or (tuple(t.shape) != shape)):
+        raise PivotError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _pages(kpages, vpages, block_table, device, d, names=("kpages", "vpages")):
+    """(num_pages, page_size, heads, max_pages) of a paged cache."""
+    for name, t in zip(names, (kpages, vpages)):
+        if t is None:
+            continue
+        _check_bf16(name, t, 4)
+        if t.device != device or t.shape[-1] != d or t.shape != kpages.shape:
+            raise PivotError(f"{name} must be [num_pages, page_size, heads, {d}] on {device}, keys and values alike")
+    n, page, H, _ = kpages.shape
+    if page < 1 or page & (page - 1):
+        raise PivotError(f"page_size must be a power of two (got {page})")
+    if n < 1 or H < 1:
+        raise PivotError("the cache has no pages or no heads")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[1] < 1:
+        raise PivotError("block_table must be an int32 tensor [B, max_pages]")
+    return n, page, H, block_table.shape[1]
+
+
+def _sequences(lead, T, cu, seqlens, block_table, device, cu_name):
+    """(B, g, pointer of cu, of seqlens, of block_table) of a call's new tokens."""
+    B = block_table.shape[0]
+    if cu is None:
+        if len(lead) != 2 or lead[0] != B:
+            raise PivotError(f"without {cu_name}, the new tokens are [B, g, heads, d] with block_table's B = {B}")
+        g, pcu = lead[1], None
+    else:
+        if len(lead) != 1:
+            raise PivotError(f"with {cu_name}, the new tokens are [T, heads, d]")
+        g, pcu = 0, _int32(cu_name, cu, device, (B + 1,))
+    return B, g, pcu, _int32("seqlens", seqlens, device, (B,)), _int32("block_table", block_table, device,
+                                                                     tuple(block_table.shape))
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=None, beta_fast=32.0,
+                     beta_slow=1.0, device="cuda"):
+    """(float64 [rot_dim / 2] radians a position, amplitude) for qk_rope and paged_append: base^(-2 i / rot_dim), with
+    the scaling for contexts beyond the trained length:
+      "none";
+      "linear": every frequency over `factor`;
+      "ntk": the base times factor^(rot_dim / (rot_dim - 2)), so the slowest pair slows down by `factor`, the fastest
+        not at all;
+      "yarn": pairs that turn fewer than beta_slow times in original_length positions over `factor`, those that turn
+        more than beta_fast times as they are, a linear mix between, and amplitude 0.1 ln(factor) + 1."""
+    if rot_dim < 16 or rot_dim % 16:
+        raise PivotError(f"rot_dim must be a positive multiple of 16 (got {rot_dim})")
+    if not (base > 1.0 and factor >= 1.0 and math.isfinite(base) and math.isfinite(factor)):
+        raise PivotError("need base > 1 and factor >= 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    amplitude = 1.0
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if original_length is None or original_length < 1 or not beta_fast > beta_slow > 0:
+            raise PivotError('"yarn" needs original_length >= 1 and beta_fast > beta_slow > 0')
+
+        def pair(turns):    # the pair that turns so many times in original_length positions
+            return rot_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rot_dim - 1)
+        mix = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        f = f / factor * mix + f * (1 - mix)
+        amplitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise PivotError('scaling must be "none", "linear", "ntk" or "yarn"')
+    return f.to(device), amplitude
+
+
+def qk_rope(q, k, positions, freqs, layout="half", amplitude=1.0, q_weight=None, k_weight=None, eps=1e-6, out_q=None,
+            out_k=None, stream=None):
+    """Norm and rotation of query and key heads in one pass, before the indexer or attention.
+
+    q, k (one may be None): bf16, fp16 or fp32 [T, heads, d] or [B, g, heads, d], d 64 or 128; views of a fused
+    projection are taken as they are.  q_weight, k_weight [d]: each head over its root mean square, times the weight.
+    positions: int32, one a token; freqs: float64 [rot_dim / 2] (rope_frequencies; None: norm only); layout: pairs
+    (i, i + rot_dim / 2) ("half") or (2 i, 2 i + 1) ("interleaved"); the channels behind rot_dim stay.  fp32
+    arithmetic, angles reduced in fp64.  Returns (q, k) in bf16, contiguous; out_q, out_k may be the bf16 inputs."""
+    lib = load_library()
+    x = q if q is not None else k
+    if x is None:
+        raise PivotError("qk_rope needs q or k")
+    lead, _, d = _tokens("q" if q is not None else "k", x)
+    device = x.device
+    _on_device(device, q=q, k=k)
+    if d not in (64, 128):
+        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
+    hq = _heads("q", q, q_weight, lead, d, x.dtype)
+    hk = _heads("k", k, k_weight, lead, d, x.dtype)
+    rope = _rope(freqs, layout, amplitude, eps, d, device)
+    T = math.prod(lead)
+    pos = None
+    if freqs is not None:
+        if positions is None or positions.numel() != T:
+            raise PivotError("positions must hold one int32 position a token")
+        pos = _int32("positions", positions, device, tuple(positions.shape))
+    sp, ctx = _where(device, stream, (q, k, positions, freqs, q_weight, k_weight, out_q, out_k))
+    with ctx:
+        out_q = _out(out_q, q.shape, torch.bfloat16, device, "out_q") if q is not None else None
+        out_k = _out(out_k, k.shape, torch.bfloat16, device, "out_k") if k is not None else None
+        if T:
+            _err(lib, lib.pivot_qk_rope(None if hq is None else ctypes.byref(hq), None if hk is None else ctypes.byref(hk),
+                                        _DTYPES[x.dtype], pos, ctypes.byref(rope), T, d, _ptr(out_q), _ptr(out_k), sp))
+    return out_q, out_k
+
+
+def paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new=None, freqs=None, layout="half", amplitude=1.0,
+                 k_weight=None, q=None, q_weight=None, eps=1e-6, out_q=None, stream=None):
+    """Writes new keys (normed and rotated as by qk_rope, at their rows' positions) and values into their pages, and
+    norms and rotates the tokens' queries in the same launch.
+
+    k, v, q: [B, g, heads, d], or [T, heads, d] with cu_new int32 [B + 1] (device; the sequences' tokens, tokens
+    behind cu_new[B] are left out); bf16, fp16 or fp32, strided views as in qk_rope; v and vpages None: a cache of
+    keys alone; q None: no queries.  kpages, vpages: bf16 [num_pages, page_size, heads, d], written in place.
+    block_table int32 [B, max_pages]; seqlens int32 [B]: each sequence's rows with the new ones, the same that the
+    indexer and the attention then take: token i of n_b goes to row seqlens[b] - n_b + i.  Returns the queries in
+    bf16 (None without q).  Sequences that do not fit their table and pages outside the cache are left out and
+    reported by sync_status()."""
+    lib = load_library()
+    lead, Hk, d = _tokens("k", k)
+    device = k.device
+    _on_device(device, v=v, q=q)
+    if (v is None) != (vpages is None):
+        raise PivotError("v and vpages go together")
+    if q is None and (out_q is not None or q_weight is not None):
+        raise PivotError("out_q and q_weight need q")
+    if d not in (64, 128):
+        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
+    hk = _heads("k", k, k_weight, lead, d, k.dtype)
+    hv = _heads("v", v, None, lead, d, k.dtype)
+    hq = _heads("q", q, q_weight, lead, d, k.dtype)
+    n, page, H, max_pages = _pages(kpages, vpages, block_table, device, d)
+    if H != Hk or (v is not None and hv.heads != Hk):
+        raise PivotError(f"k and v must have the cache's {H} heads")
+    rope = _rope(freqs, layout, amplitude, eps, d, device)
+    T = math.prod(lead)
+    B, g, pcu, psl, pbt = _sequences(lead, T, cu_new, seqlens, block_table, device, "cu_new")
+    sp, ctx = _where(device, stream, (k, v, q, kpages, vpages, block_table, seqlens, cu_new, freqs, k_weight, q_weight,
+                                      out_q))
+    with ctx:
+        out_q = _out(out_q, q.shape, torch.bfloat16, device, "out_q") if q is not None else None
+        if T and B:
+            _err(lib, lib.pivot_paged_append(ctypes.byref(hk), None if hv is None else ctypes.byref(hv),
+                                             None if hq is None else ctypes.byref(hq), _DTYPES[k.dtype],
+                                             ctypes.byref(rope), pbt, psl, pcu, T, B, d, g, n, page, max_pages,
+                                             kpages.data_ptr(), _ptr(vpages), _ptr(out_q), sp))
+    return out_q
+
+
+def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=None, scale=None, include_self=True,
+                    out=None, out_lse=None, stream=None):
+    """Dense causal attention of new tokens over the paged cache that holds their keys and values already.
+
+    q: bf16 [B, g, Hq, d] (a decode step), or [T, Hq, d] with cu_q int32 [B + 1] (chunks of any lengths; rows of
+    tokens behind cu_q[B] are left as they were); Hq a multiple of the cache's heads, query head h reads key head
+    h // (Hq // Hk).  Token i of n_b sits at position seqlens[b] - n_b + i and sees the keys up to its own, or, with
+    include_self=False, those before it (the indexer's keys); a query that sees none gets zeros and lse -inf.
+    max_seqlen bounds seqlens.  scale: d ** -0.5 by default.  out_lse: float32 [..., Hq], the log of each row's sum.
+    Returns bf16 with q's shape."""
+    lib = load_library()
+    _check_bf16("q", q, q.dim())
+    lead, Hq, d = _tokens("q", q)
+    device = q.device
+    if d not in (64, 128):
+        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
+    n, page, Hk, max_pages = _pages(kpages, vpages, block_table, device, d)
+    if Hq % Hk or Hq < 1:
+        raise PivotError(f"q's heads must be a multiple of the cache's {Hk} (got {Hq})")
+    T = math.prod(lead)
+    B, g, pcu, psl, pbt = _sequences(lead, T, cu_q, seqlens, block_table, device, "cu_q")
+    max_seqlen = int(max_seqlen)
+    opt = _Attend(d ** -0.5 if scale is None else float(scale), 1 if include_self else 0)
+    sp, ctx = _where(device, stream, (q, kpages, vpages, block_table, seqlens, cu_q, out, out_lse))
+    with ctx:
+        out = _out(out, q.shape, torch.bfloat16, device, "out")
+        if out_lse is not None:
+            _out(out_lse, q.shape[:-1], torch.float32, device, "out_lse")
+        if T and B:
+            nbytes = lib.pivot_paged_attention_workspace_size(T, B, Hq, Hk, d, max_seqlen)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+            _err(lib, lib.pivot_paged_attention(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pcu,
+                                                ctypes.byref(opt), T, B, Hq, Hk, d, g, n, page, max_pages, max_seqlen,
+                                                out.data_ptr(), _ptr(out_lse), _ptr(ws), nbytes, sp))
+    return out
+
+
+def sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out=None, stream=None):
+    """sparse_attention over the paged cache: q bf16 [B, g, H, d], idx int32 [B, g, H, top_k] (the rows of
+    pivot_decode_index_paged), kpages and vpages with q's H heads.  Returns float32 [B, g, H, d].  Indices at or
+    beyond seqlens[b] and pages outside the cache are left out and reported by sync_status()."""
+    lib = load_library()
+    _check_bf16("q", q, 4)
+    lead, H, d = _tokens("q", q)
+    device = q.device
+    if d not in (64, 128):
+        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
+    n, page, Hk, max_pages = _pages(kpages, vpages, block_table, device, d)
+    if Hk != H:
+        raise PivotError(f"q must have the cache's {Hk} heads (got {H})")
+    B, g, _, psl, pbt = _sequences(lead, lead[0] * lead[1], None, seqlens, block_table, device, "cu_q")
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 4:
+        raise PivotError("idx must be an int32 tensor [B, g, H, top_k]")
+    pidx = _int32("idx", idx, device, (B, g, H, idx.shape[-1]))
+    sp, ctx = _where(device, stream, (q, kpages, vpages, block_table, seqlens, idx, out))
+    with ctx:
+        out = _out(out, q.shape, torch.float32, device, "out")
+        if idx.numel():
+            _err(lib, lib.pivot_sparse_attention_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl,
+                                                       pidx, B, H, d, g, n, page, max_pages, idx.shape[-1],
+                                                       out.data_ptr(), sp))
+        else:
+            out.zero_()
     return out
 
 

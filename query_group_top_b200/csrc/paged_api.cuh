@@ -1,0 +1,265 @@
+// Host side of the serving step over a paged cache: argument checks, the split
+// of the key axis and the launches of pivot_qk_rope, pivot_paged_append,
+// pivot_paged_attention and pivot_sparse_attention_paged.  Part of pivot.cu,
+// whose helpers it uses.
+#pragma once
+
+namespace {
+
+size_t dtype_bytes(int t) { return t == PIVOT_FP32 ? 4 : 2; }
+
+int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+// Heads that rope_kernel reads: 16-byte rows of d channels at strides that keep them aligned.
+int head_rows(const char* name, const pivot_heads_t* h, int dtype, HeadRows* out) {
+  *out = HeadRows{};
+  if (!h) return PIVOT_OK;
+  if (!h->data || h->heads < 1) return fail(PIVOT_ERR_INVALID_ARG, "%s: null data or no heads", name);
+  const long long step = 16 / static_cast<long long>(dtype_bytes(dtype));
+  if (!aligned16(h->data) || (h->weight && !aligned16(h->weight)) || h->token_stride % step || h->head_stride % step)
+    return fail(PIVOT_ERR_INVALID_ARG, "%s: rows must start on 16-byte boundaries", name);
+  *out = HeadRows{h->data, h->weight, h->token_stride, h->head_stride, h->heads};
+  return PIVOT_OK;
+}
+
+int paged_rows(const int32_t* block_table, const int32_t* seqlens, const int32_t* cu, int T, int B, int g,
+               int num_pages, int page_size, int max_pages, int max_seqlen, PagedRows* out) {
+  if (!block_table || !seqlens) return fail(PIVOT_ERR_INVALID_ARG, "null block_table or seqlens");
+  if (T < 1 || B < 1) return fail(PIVOT_ERR_INVALID_ARG, "need T >= 1 and B >= 1");
+  if (!cu && (g < 1 || static_cast<long long>(B) * g != T))
+    return fail(PIVOT_ERR_INVALID_ARG, "without cu offsets every sequence has g >= 1 new tokens and T = B * g");
+  if (page_size < 1 || page_size > (1 << 24) || (page_size & (page_size - 1)) != 0)
+    return fail(PIVOT_ERR_INVALID_ARG, "page_size must be a power of two (got %d)", page_size);
+  if (num_pages < 1 || max_pages < 1 || max_seqlen < 1)
+    return fail(PIVOT_ERR_INVALID_ARG, "need num_pages, max_pages, max_seqlen >= 1");
+  const int lg = log2_of(page_size);
+  *out = PagedRows{block_table, seqlens, cu, B, T, g, max_pages, num_pages, lg, paged_max_len(max_pages, lg, max_seqlen)};
+  return PIVOT_OK;
+}
+
+template <int D, class T>
+int launch_rope(const RopeParams& rp, bool half, int grid, cudaStream_t st) {
+  TraceScope tr(rp.kpages ? "paged_append" : "qk_rope", st);
+  if (half)
+    rope_kernel<D, true, T><<<grid, kRopeNT, 0, st>>>(rp);
+  else
+    rope_kernel<D, false, T><<<grid, kRopeNT, 0, st>>>(rp);
+  CUDA_TRY(cudaGetLastError());
+  return PIVOT_OK;
+}
+
+int run_rope(RopeParams rp, int dtype, const pivot_rope_t* rope, int d, cudaStream_t st) {
+  if (d != 64 && d != 128) return fail(PIVOT_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
+  const bool turned = rope && rope->freqs;
+  rp.rot = turned ? rope->rot_dim : 0;
+  if (turned && (rp.rot < 16 || rp.rot > d || rp.rot % 16))
+    return fail(PIVOT_ERR_INVALID_ARG, "rot_dim must be a multiple of 16 in [16, d] (got %d)", rp.rot);
+  if (turned && rope->layout != PIVOT_ROPE_HALF && rope->layout != PIVOT_ROPE_INTERLEAVED)
+    return fail(PIVOT_ERR_INVALID_ARG, "layout must be PIVOT_ROPE_HALF or PIVOT_ROPE_INTERLEAVED");
+  if (turned && (reinterpret_cast<uintptr_t>(rope->freqs) & 7))
+    return fail(PIVOT_ERR_INVALID_ARG, "freqs must be 8-byte aligned");
+  rp.amplitude = turned ? static_cast<float>(rope->amplitude) : 1.f;
+  rp.eps = rope ? static_cast<float>(rope->eps) : 0.f;
+  rp.freqs = turned ? rope->freqs : nullptr;
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  rp.status = dev->status;
+  // A block's groups of d/16 lanes take a head each.  Few tokens: one a block,
+  // for the latency; many: as many as give each group some four heads, so that
+  // the cosines' cost is spread and the loads of one head hide the next.
+  const int heads = rp.q.n + rp.k.n + rp.v.n, groups = kRopeNT / (d / 16);
+  int tb = std::min(kRopeMaxTok, std::max(1, 4 * groups / heads));
+  while (tb > 1 && (rp.T + tb - 1) / tb < 2 * dev->sms) tb >>= 1;
+  rp.tokens_per_block = tb;
+  const int grid = (rp.T + tb - 1) / tb;
+  const bool half = !turned || rope->layout == PIVOT_ROPE_HALF;
+  if (dtype == PIVOT_BF16)
+    return d == 128 ? launch_rope<128, __nv_bfloat16>(rp, half, grid, st) : launch_rope<64, __nv_bfloat16>(rp, half, grid, st);
+  if (dtype == PIVOT_FP16)
+    return d == 128 ? launch_rope<128, __half>(rp, half, grid, st) : launch_rope<64, __half>(rp, half, grid, st);
+  return d == 128 ? launch_rope<128, float>(rp, half, grid, st) : launch_rope<64, float>(rp, half, grid, st);
+}
+
+int check_dtype(int dtype) {
+  if (dtype != PIVOT_BF16 && dtype != PIVOT_FP16 && dtype != PIVOT_FP32)
+    return fail(PIVOT_ERR_INVALID_ARG, "dtype must be PIVOT_BF16, PIVOT_FP16 or PIVOT_FP32");
+  return PIVOT_OK;
+}
+
+// How paged attention splits the key axis.
+struct AttendPlan {
+  int nsplit;
+  size_t part_lse, total;   // workspace: the parts' rows at 0, their lse at part_lse
+};
+
+AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int sms) {
+  AttendPlan a{};
+  const long long tiles = std::max<long long>(B, (static_cast<long long>(T) * (Hq / Hk) + 15) / 16);
+  const long long want = static_cast<long long>(sms) * 2 * 4;   // four rounds of two CTAs an SM
+  long long n = std::max<long long>(1, want / (tiles * Hk));
+  a.nsplit = static_cast<int>(std::min<long long>(n, (max_seqlen + kMinChunk - 1) / kMinChunk));
+  if (a.nsplit > 1) {
+    const size_t rows = static_cast<size_t>(a.nsplit) * T * Hq;
+    a.part_lse = up(rows * d * sizeof(float));
+    a.total = a.part_lse + up(rows * sizeof(float));
+  }
+  return a;
+}
+
+template <int D>
+int launch_attend(const PagedAttendParams& ap, cudaStream_t st) {
+  const long long grid = static_cast<long long>(ap.tiles) * ap.Hk * ap.nsplit;
+  CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::SMEM));
+  {
+    TraceScope tr("attend_rows", st);
+    attend_rows_kernel<D><<<static_cast<unsigned>(grid), 128, RowsCfg<D>::SMEM, st>>>(ap);
+  }
+  CUDA_TRY(cudaGetLastError());
+  if (ap.nsplit > 1) {
+    TraceScope tr("attend_join", st);
+    const long long rows = static_cast<long long>(ap.rows.T) * ap.Hq;
+    attend_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(ap);
+  }
+  CUDA_TRY(cudaGetLastError());
+  return PIVOT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pivot_qk_rope(const pivot_heads_t* q, const pivot_heads_t* k, int dtype, const int32_t* positions,
+                  const pivot_rope_t* rope, int T, int d, void* out_q, void* out_k, void* stream) {
+  RopeParams rp{};
+  if (int rc = check_dtype(dtype)) return rc;
+  if (int rc = head_rows("q", q, dtype, &rp.q)) return rc;
+  if (int rc = head_rows("k", k, dtype, &rp.k)) return rc;
+  if (T < 1) return fail(PIVOT_ERR_INVALID_ARG, "T must be >= 1");
+  if ((!q && !k) || (q && !out_q) || (k && !out_k)) return fail(PIVOT_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned16(out_q) || !aligned16(out_k)) return fail(PIVOT_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  if (rope && rope->freqs && !positions) return fail(PIVOT_ERR_INVALID_ARG, "a rotation needs positions");
+  rp.positions = positions;
+  rp.out_q = static_cast<uint16_t*>(out_q);
+  rp.out_k = static_cast<uint16_t*>(out_k);
+  rp.T = T;
+  return run_rope(rp, dtype, rope, d, static_cast<cudaStream_t>(stream));
+}
+
+int pivot_paged_append(const pivot_heads_t* k, const pivot_heads_t* v, const pivot_heads_t* q, int dtype,
+                       const pivot_rope_t* rope, const int32_t* block_table, const int32_t* seqlens,
+                       const int32_t* cu_new, int T, int B, int d, int g, int num_pages, int page_size, int max_pages,
+                       void* kpages, void* vpages, void* out_q, void* stream) {
+  RopeParams rp{};
+  if (int rc = check_dtype(dtype)) return rc;
+  if (!k || !kpages || (v && !vpages) || (q && !out_q)) return fail(PIVOT_ERR_INVALID_ARG, "null tensor pointer");
+  if (int rc = head_rows("k", k, dtype, &rp.k)) return rc;
+  if (int rc = head_rows("v", v, dtype, &rp.v)) return rc;
+  if (int rc = head_rows("q", q, dtype, &rp.q)) return rc;
+  if (v && v->heads != k->heads) return fail(PIVOT_ERR_INVALID_ARG, "k and v must have the same heads");
+  if (v && v->weight) return fail(PIVOT_ERR_INVALID_ARG, "values take no norm weight");
+  if (!aligned16(kpages) || !aligned16(vpages) || !aligned16(out_q))
+    return fail(PIVOT_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  if (int rc = paged_rows(block_table, seqlens, cu_new, T, B, g, num_pages, page_size, max_pages, 0x7FFFFFFF, &rp.rows))
+    return rc;
+  rp.out_q = static_cast<uint16_t*>(out_q);
+  rp.kpages = static_cast<uint16_t*>(kpages);
+  rp.vpages = static_cast<uint16_t*>(vpages);
+  rp.T = T;
+  return run_rope(rp, dtype, rope, d, static_cast<cudaStream_t>(stream));
+}
+
+size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int max_seqlen) {
+  if (T < 1 || B < 1 || Hk < 1 || Hq < Hk || d < 1 || max_seqlen < 1) return 0;
+  return plan_attend(T, B, Hq, Hk, d, max_seqlen, device_sms()).total;
+}
+
+int pivot_paged_attention(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
+                          const int32_t* seqlens, const int32_t* cu_q, const pivot_attend_t* options, int T, int B,
+                          int Hq, int Hk, int d, int g, int num_pages, int page_size, int max_pages, int max_seqlen,
+                          void* out, float* out_lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !kpages || !vpages || !out) return fail(PIVOT_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned16(q) || !aligned16(kpages) || !aligned16(vpages) || !aligned16(out))
+    return fail(PIVOT_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (d != 64 && d != 128) return fail(PIVOT_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
+  if (Hk < 1 || Hq < Hk || Hq % Hk)
+    return fail(PIVOT_ERR_INVALID_ARG, "query heads must be a multiple of the key heads (Hq=%d, Hk=%d)", Hq, Hk);
+  PagedAttendParams ap{};
+  if (int rc = paged_rows(block_table, seqlens, cu_q, T, B, g, num_pages, page_size, max_pages, max_seqlen, &ap.rows))
+    return rc;
+  if (max_seqlen >= (1 << 30)) return fail(PIVOT_ERR_INVALID_ARG, "max_seqlen too large");
+  const double scale = options ? options->scale : 1.0 / sqrt(static_cast<double>(d));
+  if (!(scale > 0.0) || !(scale < 1e30)) return fail(PIVOT_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (static_cast<long long>(T) * (Hq / Hk) >= (1ll << 31) - 32) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  const AttendPlan pl = plan_attend(T, B, Hq, Hk, d, max_seqlen, dev->sms);
+  if (pl.total > workspace_bytes || (pl.total && !workspace))
+    return fail(PIVOT_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", pl.total, workspace_bytes);
+  if (pl.total && (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+    return fail(PIVOT_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  ap.q = static_cast<const uint16_t*>(q);
+  ap.kpages = static_cast<const uint16_t*>(kpages);
+  ap.vpages = static_cast<const uint16_t*>(vpages);
+  ap.Hq = Hq;
+  ap.Hk = Hk;
+  ap.grp = Hq / Hk;
+  ap.self_key = options ? (options->include_self != 0) : 1;
+  ap.nsplit = pl.nsplit;
+  const long long tiles = cu_q ? (static_cast<long long>(T) * ap.grp + 15) / 16 + B
+                               : static_cast<long long>(B) * ((static_cast<long long>(g) * ap.grp + 15) / 16);
+  if (tiles * Hk * pl.nsplit >= (1ll << 31)) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
+  ap.tiles = static_cast<int>(tiles);
+  ap.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  ap.out = static_cast<uint16_t*>(out);
+  ap.lse = out_lse;
+  ap.part_o = static_cast<float*>(workspace);
+  ap.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part_lse);
+  ap.status = dev->status;
+  ap.wait_ns = wait_limit_ns();
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_attend<128>(ap, st) : launch_attend<64>(ap, st);
+}
+
+int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
+                                 const int32_t* seqlens, const int32_t* idx, int B, int H, int d, int g, int num_pages,
+                                 int page_size, int max_pages, int top_k, float* out, void* stream) {
+  if (!q || !kpages || !vpages || !idx || !out) return fail(PIVOT_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned16(q) || !aligned16(kpages) || !aligned16(vpages) || !aligned16(idx) || !aligned16(out))
+    return fail(PIVOT_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  if (d != 64 && d != 128) return fail(PIVOT_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
+  if (B < 1 || g < 1 || H < 1 || top_k < 1) return fail(PIVOT_ERR_INVALID_ARG, "need B, g, H, top_k >= 1");
+  if (static_cast<double>(B) * g * H >= 2147483648.0) return fail(PIVOT_ERR_INVALID_ARG, "B * g * H too large");
+  AttendParams ap{};
+  if (int rc = paged_rows(block_table, seqlens, nullptr, B * g, B, g, num_pages, page_size, max_pages, 0x7FFFFFFF, &ap.rows))
+    return rc;
+  DeviceInfo* dev = nullptr;
+  if (int rc = device_info(&dev)) return rc;
+  ap.q = static_cast<const uint16_t*>(q);
+  ap.k = static_cast<const uint16_t*>(kpages);
+  ap.v = static_cast<const uint16_t*>(vpages);
+  ap.idx = idx;
+  ap.out = out;
+  ap.R = B * g;
+  ap.H = H;
+  ap.g = g;
+  ap.top_k = top_k;
+  ap.scale = 1.0f / sqrtf(static_cast<float>(d));
+  ap.status = dev->status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    TraceScope tr("sparse_attention", st);
+    const unsigned grid = static_cast<unsigned>(static_cast<long long>(ap.R) * H);
+    if (d == 128)
+      sparse_attention_kernel<128, true><<<grid, kAttNT, 0, st>>>(ap);
+    else
+      sparse_attention_kernel<64, true><<<grid, kAttNT, 0, st>>>(ap);
+  }
+  CUDA_TRY(cudaGetLastError());
+  return PIVOT_OK;
+}
+
+}  // extern "C"

@@ -12,6 +12,7 @@
 // Decode (pivot_decode_index): proxy_kernel -> decode_scan_kernel ->
 // decode_select_kernel -> refine_kernel.
 // Consumer (pivot_sparse_attention): sparse_attention_kernel over index rows.
+// The serving step around them (paged_api.cuh): rope_kernel, attend_*_kernel.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -26,9 +27,11 @@
 #include "../../include/pivot.h"
 #include "attend.cuh"
 #include "finalize.cuh"
+#include "paged_attend.cuh"
 #include "proxy_decode.cuh"
 #include "ptx.cuh"
 #include "refine.cuh"
+#include "rope.cuh"
 #include "scan.cuh"
 
 namespace {
@@ -637,6 +640,8 @@ int device_sms() {
 
 }  // namespace
 
+#include "paged_api.cuh"
+
 // ---------------------------------------------------------------- no-allocation decode
 // Scratch for pivot_decode_index_noalloc: a fixed device array that every GPU
 // loading this library holds until the process exits.  Host code must not pass
@@ -792,9 +797,9 @@ int pivot_sparse_attention(const void* q, const void* k, const void* v, const in
     TraceScope tr("sparse_attention", st);
     const unsigned grid = static_cast<unsigned>(static_cast<long long>(R) * H);
     if (d == 128)
-      sparse_attention_kernel<128><<<grid, kAttNT, 0, st>>>(ap);
+      sparse_attention_kernel<128, false><<<grid, kAttNT, 0, st>>>(ap);
     else
-      sparse_attention_kernel<64><<<grid, kAttNT, 0, st>>>(ap);
+      sparse_attention_kernel<64, false><<<grid, kAttNT, 0, st>>>(ap);
   }
   CUDA_TRY(cudaGetLastError());
   return PIVOT_OK;
@@ -846,6 +851,8 @@ int pivot_sync_status(void* stream, int* flags) {
   if (flags) *flags = v;
   if (v & kStTimeout) return fail(PIVOT_ERR_TIMEOUT, "a kernel wait timed out; outputs of that call are invalid");
   if (v & kStBadLen) return fail(PIVOT_ERR_INVALID_ARG, "a decode sequence was longer than max_seqlen");
+  if (v & kStBadPage)
+    return fail(PIVOT_ERR_INVALID_ARG, "a block table named a page outside the cache, or an index a row outside its sequence");
   if (v & kStNoConverge) return fail(PIVOT_ERR_CUDA, "a refine selection did not converge; outputs of that call are invalid");
   return PIVOT_OK;
 }

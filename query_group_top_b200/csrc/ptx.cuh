@@ -16,6 +16,7 @@ enum : int {
   kStBadLen = 2,    // a decode sequence was longer than the declared maximum
   kStFallback = 4,  // informational: some rows took the exact fallback path
   kStNoConverge = 8,  // a selection exceeded its round limit (cannot happen on finite scores)
+  kStBadPage = 16,    // a block table named a page outside the cache, or an index a row outside its sequence
 };
 
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s: the default limit of a wait
