@@ -108,7 +108,7 @@ def load_library():
         "pivot_set_wait_limit": ([ctypes.c_ulonglong], I),
         "pivot_qk_rope": ([P, P, I, P, P, I, I, P, P, P], I),
         "pivot_paged_append": ([P, P, P, I, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P], I),
-        "pivot_paged_attention_workspace_size": ([I, I, I, I, I, I], Z),
+        "pivot_paged_attention_workspace_size": ([I, I, I, I, I, I, I], Z),
         "pivot_paged_attention": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P, P, Z, P], I),
         "pivot_sparse_attention_paged": ([P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P], I),
     }
@@ -616,7 +616,7 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
         if out_lse is not None:
             _out(out_lse, q.shape[:-1], torch.float32, device, "out_lse")
         if T and B:
-            nbytes = lib.pivot_paged_attention_workspace_size(T, B, Hq, Hk, d, max_seqlen)
+            nbytes = lib.pivot_paged_attention_workspace_size(T, B, Hq, Hk, d, page, max_seqlen)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
             _err(lib, lib.pivot_paged_attention(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pcu,
                                                 ctypes.byref(opt), T, B, Hq, Hk, d, g, n, page, max_pages, max_seqlen,

@@ -34,6 +34,8 @@ int paged_rows(const int32_t* block_table, const int32_t* seqlens, const int32_t
     return fail(PIVOT_ERR_INVALID_ARG, "without cu offsets every sequence has g >= 1 new tokens and T = B * g");
   if (page_size < 1 || page_size > (1 << 24) || (page_size & (page_size - 1)) != 0)
     return fail(PIVOT_ERR_INVALID_ARG, "page_size must be a power of two (got %d)", page_size);
+  if (static_cast<long long>(num_pages) * page_size >= (1ll << 31))
+    return fail(PIVOT_ERR_INVALID_ARG, "the cache has too many rows");
   if (num_pages < 1 || max_pages < 1 || max_seqlen < 1)
     return fail(PIVOT_ERR_INVALID_ARG, "need num_pages, max_pages, max_seqlen >= 1");
   const int lg = log2_of(page_size);
@@ -90,33 +92,48 @@ int check_dtype(int dtype) {
   return PIVOT_OK;
 }
 
-// How paged attention splits the key axis.
+// Which kernel takes a call of paged attention, and how the key axis is split.
 struct AttendPlan {
-  int nsplit;
+  bool tiles;               // attend_tiles_kernel, else attend_rows_kernel
+  int rows;                 // packed rows of a CTA
+  int nsplit, min_chunk;
   size_t part_lse, total;   // workspace: the parts' rows at 0, their lse at part_lse
 };
 
-AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int sms) {
+AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int page_size, int max_seqlen, int sms) {
   AttendPlan a{};
-  const long long tiles = std::max<long long>(B, (static_cast<long long>(T) * (Hq / Hk) + 15) / 16);
-  const long long want = static_cast<long long>(sms) * 2 * 4;   // four rounds of two CTAs an SM
-  long long n = std::max<long long>(1, want / (tiles * Hk));
-  a.nsplit = static_cast<int>(std::min<long long>(n, (max_seqlen + kMinChunk - 1) / kMinChunk));
+  const long long rows = static_cast<long long>(T) * (Hq / Hk);
+  // TMA lays boxes of 8 rows or more into the swizzled tiles, so smaller pages go to the rows kernel
+  a.tiles = rows >= 32ll * B && page_size >= 8;
+  a.rows = a.tiles ? 256 : 16;
+  a.min_chunk = a.tiles ? 512 : 256;
+  const long long ctas = std::max<long long>(B, (rows + a.rows - 1) / a.rows) * Hk;
+  const long long want = a.tiles ? 2ll * sms : 8ll * sms;   // two rounds of one CTA an SM; four of two
+  const long long n = std::max<long long>(1, want / ctas);
+  a.nsplit = static_cast<int>(std::min<long long>(n, (max_seqlen + a.min_chunk - 1) / a.min_chunk));
   if (a.nsplit > 1) {
-    const size_t rows = static_cast<size_t>(a.nsplit) * T * Hq;
-    a.part_lse = up(rows * d * sizeof(float));
-    a.total = a.part_lse + up(rows * sizeof(float));
+    const size_t parts = static_cast<size_t>(a.nsplit) * T * Hq;
+    a.part_lse = up(parts * d * sizeof(float));
+    a.total = a.part_lse + up(parts * sizeof(float));
   }
   return a;
 }
 
 template <int D>
-int launch_attend(const PagedAttendParams& ap, cudaStream_t st) {
-  const long long grid = static_cast<long long>(ap.tiles) * ap.Hk * ap.nsplit;
-  CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::SMEM));
-  {
+int launch_attend(const PagedAttendParams& ap, bool tiles, int box_rows, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(static_cast<long long>(ap.tiles) * ap.Hk * ap.nsplit);
+  if (tiles) {
+    CUtensorMap mk, mv;
+    const int rows = ap.rows.num_pages << ap.rows.log2_page;
+    if (int rc = make_rows_map(&mk, ap.kpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
+    if (int rc = make_rows_map(&mv, ap.vpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
+    CUDA_TRY(cudaFuncSetAttribute(attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::SMEM));
+    TraceScope tr("attend_tiles", st);
+    attend_tiles_kernel<D><<<grid, TcCfg<D>::THREADS, TcCfg<D>::SMEM, st>>>(mk, mv, ap);
+  } else {
+    CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::SMEM));
     TraceScope tr("attend_rows", st);
-    attend_rows_kernel<D><<<static_cast<unsigned>(grid), 128, RowsCfg<D>::SMEM, st>>>(ap);
+    attend_rows_kernel<D><<<grid, 128, RowsCfg<D>::SMEM, st>>>(ap);
   }
   CUDA_TRY(cudaGetLastError());
   if (ap.nsplit > 1) {
@@ -172,9 +189,9 @@ int pivot_paged_append(const pivot_heads_t* k, const pivot_heads_t* v, const piv
   return run_rope(rp, dtype, rope, d, static_cast<cudaStream_t>(stream));
 }
 
-size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int max_seqlen) {
-  if (T < 1 || B < 1 || Hk < 1 || Hq < Hk || d < 1 || max_seqlen < 1) return 0;
-  return plan_attend(T, B, Hq, Hk, d, max_seqlen, device_sms()).total;
+size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int page_size, int max_seqlen) {
+  if (T < 1 || B < 1 || Hk < 1 || Hq < Hk || d < 1 || page_size < 1 || max_seqlen < 1) return 0;
+  return plan_attend(T, B, Hq, Hk, d, page_size, max_seqlen, device_sms()).total;
 }
 
 int pivot_paged_attention(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
@@ -196,7 +213,7 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   if (static_cast<long long>(T) * (Hq / Hk) >= (1ll << 31) - 32) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
   DeviceInfo* dev = nullptr;
   if (int rc = device_info(&dev)) return rc;
-  const AttendPlan pl = plan_attend(T, B, Hq, Hk, d, max_seqlen, dev->sms);
+  const AttendPlan pl = plan_attend(T, B, Hq, Hk, d, page_size, max_seqlen, dev->sms);
   if (pl.total > workspace_bytes || (pl.total && !workspace))
     return fail(PIVOT_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", pl.total, workspace_bytes);
   if (pl.total && (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
@@ -209,8 +226,9 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   ap.grp = Hq / Hk;
   ap.self_key = options ? (options->include_self != 0) : 1;
   ap.nsplit = pl.nsplit;
-  const long long tiles = cu_q ? (static_cast<long long>(T) * ap.grp + 15) / 16 + B
-                               : static_cast<long long>(B) * ((static_cast<long long>(g) * ap.grp + 15) / 16);
+  ap.min_chunk = pl.min_chunk;
+  const long long tiles = cu_q ? (static_cast<long long>(T) * ap.grp + pl.rows - 1) / pl.rows + B
+                               : B * ((static_cast<long long>(g) * ap.grp + pl.rows - 1) / pl.rows);
   if (tiles * Hk * pl.nsplit >= (1ll << 31)) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
   ap.tiles = static_cast<int>(tiles);
   ap.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
@@ -221,7 +239,8 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   ap.status = dev->status;
   ap.wait_ns = wait_limit_ns();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_attend<128>(ap, st) : launch_attend<64>(ap, st);
+  const int box = std::min(page_size, 128);
+  return d == 128 ? launch_attend<128>(ap, pl.tiles, box, st) : launch_attend<64>(ap, pl.tiles, box, st);
 }
 
 int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,

@@ -34,7 +34,7 @@ struct PagedAttendParams {
   PagedRows rows;
   int Hq, Hk, grp;         // grp = Hq / Hk
   int self_key;            // 1: a query sees its own key
-  int nsplit;              // CTAs along the keys of each row tile
+  int nsplit, min_chunk;   // CTAs along the keys of each row tile; the fewest keys that a part is worth
   int tiles;               // row tiles over all sequences (an upper bound where cu is given)
   float scale_log2;        // scale * log2(e)
   uint16_t* out;           // [T][Hq][d] bf16
@@ -48,11 +48,9 @@ struct PagedAttendParams {
 constexpr float kLn2 = 0.693147180559945309f;
 
 // Keys per part of a sequence of `len` rows: an nsplit-th of it, whatever the
-// bound that sized the grid, in whole 64-key runs, and no less than 256 keys
-// (a part costs some 2 us before its first key arrives).
-constexpr int kMinChunk = 256;
-__device__ __forceinline__ int chunk_of(int len, int nsplit) {
-  return max(kMinChunk, ((len + nsplit - 1) / nsplit + 63) & ~63);
+// bound that sized the grid, in whole 128-key tiles, and no less than min_chunk.
+__device__ __forceinline__ int chunk_of(int len, const PagedAttendParams& p) {
+  return max(p.min_chunk, ((len + p.nsplit - 1) / p.nsplit + 127) & ~127);
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -200,7 +198,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
     return (static_cast<long long>(sp.tok0) + (r0 + r) / p.grp) * p.Hq + hk * p.grp + (r0 + r) % p.grp;
   };
   if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
-  const int chunk = chunk_of(sp.len, p.nsplit);
+  const int chunk = chunk_of(sp.len, p);
   const int kbeg = split * chunk;
   const int kend = min(lim_of(nrows - 1), kbeg + chunk);
   if (kbeg >= kend && split > 0) return;                   // the join reads no part a row has no keys in
@@ -396,7 +394,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const NewSpan sp = p.rows.span(find_sequence(p.rows, tok, lane));
   if (tok < sp.tok0 || tok >= sp.tok0 + sp.n) return;
   const int lim = sp.ok ? sp.len - sp.n + p.self_key + (tok - sp.tok0) : 0;
-  const int chunk = chunk_of(sp.len, p.nsplit);
+  const int chunk = chunk_of(sp.len, p);
   const int parts = max(1, (lim + chunk - 1) / chunk);
   float m = neg_inf();
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_lse[s * rows + row]);

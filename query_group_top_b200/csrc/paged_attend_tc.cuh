@@ -1,0 +1,431 @@
+// Dense causal attention over a paged cache for many rows per key head, on the
+// 5th-generation tensor cores.  The mathematics and the packing of rows are
+// those of paged_attend.cuh.
+//
+// A CTA takes 256 packed rows (two tiles of 128) of one key head and walks the
+// key axis in tiles of 128 keys:
+//   warp 0      producer: looks each tile's pages up in the block table and
+//               brings keys and values in by TMA, one box per page and 64
+//               channels (a page of 128 rows or more: per tile), through one
+//               ring of key and value tiles
+//   warp 1      TMEM allocator and MMA issuer (one elected thread):
+//               S_t = Q_t K^T (128 x 128 x d), O_t += P_t V (128 x d x 128),
+//               P_t read from TMEM, V as it lies (keys in rows: N-major)
+//   warps 2-5, 6-9  softmax of tile 0 and tile 1: thread = row.  128 scores in
+//               registers, so maximum and sum need no exchange; P_t goes back to
+//               TMEM in bf16 over the scores it came from
+// While one tile's softmax runs, the tensor cores work for the other.  TMEM:
+// S_0, S_1 (128 columns each), O_0, O_1 (d each).
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 since the
+// last time (the row's reference stays behind its maximum, the weights then
+// reach up to 2^8, which fp32 sums and bf16 weights hold as exactly as those up
+// to 1); after the first tiles this hardly ever happens, and the four passes of
+// O through the registers are saved.  The score tile's commit also tells that
+// the earlier P V product is done (one thread issues both), so the softmax
+// warps may change O between it and their own arrival.
+#pragma once
+
+#include "paged_attend.cuh"
+
+namespace pivot {
+
+template <int D>
+struct TcCfg {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int ATOMS = D / 64;                   // 64-channel halves of a row
+  static constexpr int TILE = BN * D * 2;                // a key, value or query tile
+  static constexpr int ATOM = BN * 128;                  // one half of it
+  static constexpr int NST = D == 128 ? 5 : 8;           // ring of key and value tiles
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_RING + NST * TILE;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;      // barriers, alignment slack
+  static constexpr int THREADS = 64 + 256;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;      // + t * 128, + t * D
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SMEM > 116 * 1024, "one CTA an SM: each takes the whole TMEM");
+};
+
+constexpr float kRescaleLog2 = 8.f;
+
+template <int D>
+__global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
+attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ PagedAttendParams p) {
+  using C = TcCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t ring = sbase + C::OFF_RING;
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::NST + s); };
+  constexpr int B0 = 2 * C::NST;
+  const uint32_t q_bar = bar0 + 8u * B0;
+  auto s_bar = [&](int t) { return bar0 + 8u * (B0 + 1 + t); };    // scores of tile t are in TMEM
+  auto p_bar = [&](int t) { return bar0 + 8u * (B0 + 3 + t); };    // weights of tile t are in TMEM
+  auto o_bar = [&](int t) { return bar0 + 8u * (B0 + 5 + t); };    // the last product of tile t is done
+  const uint32_t tail_bar = bar0 + 8u * (B0 + 7);
+  const uint32_t done_bar = bar0 + 8u * (B0 + 8);
+  static_assert(8 * (2 * C::NST + 9) <= 224, "barriers");
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 224);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 228);
+  int* seq_s = reinterpret_cast<int*>(smem + C::OFF_BAR + 232);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // key heads innermost (neighbouring CTAs share pages), the longest row tiles first
+  const long long bid = blockIdx.x;
+  const int hk = static_cast<int>(bid % p.Hk);
+  const int split = static_cast<int>(bid / p.Hk % p.nsplit);
+  const int flat = p.tiles - 1 - static_cast<int>(bid / p.Hk / p.nsplit);
+  if (warp == 0) {
+    int tile = 0;
+    const int b = locate_tile(p.rows, p.grp, 2 * C::BM, flat, lane, &tile, p.status);
+    if (lane == 0) {
+      seq_s[0] = b;
+      seq_s[1] = tile;
+      for (int s = 0; s < C::NST; ++s) {
+        mbar_init(full_bar(s), 1);
+        mbar_init(empty_bar(s), 1);
+      }
+      mbar_init(q_bar, 256);
+      for (int t = 0; t < 2; ++t) {
+        mbar_init(s_bar(t), 1);
+        mbar_init(p_bar(t), 128);
+        mbar_init(o_bar(t), 1);
+      }
+      mbar_init(tail_bar, 1);
+      mbar_init(done_bar, 1);
+      *abort_flag = 0;
+      fence_barrier_init();
+    }
+  }
+  __syncthreads();
+  const int b = seq_s[0], r0 = seq_s[1] * (2 * C::BM);
+  if (b < 0) return;
+  const NewSpan sp = p.rows.span(b);
+  const int total = sp.n * p.grp;                           // packed rows of the sequence
+  if (r0 >= total) return;
+  if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
+  const int pos0 = sp.len - sp.n + p.self_key;
+  auto lim_of = [&](int r) { return sp.ok ? pos0 + r / p.grp : 0; };
+  const int chunk = chunk_of(sp.len, p);
+  const int kbeg = split * chunk;
+  // keys of the part that the last row of tile t sees; its key tiles
+  int kend[2], nk[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int first = r0 + t * C::BM, last = min(first + C::BM, total) - 1;
+    kend[t] = first < total ? min(lim_of(last), kbeg + chunk) : 0;
+    nk[t] = max(0, (kend[t] - kbeg + C::BN - 1) / C::BN);
+  }
+  const int n = max(nk[0], nk[1]);
+  if (n == 0 && split > 0) return;                          // the join reads no part a row has no keys in
+
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int end = max(kend[0], kend[1]);
+    const int page_rows = min(1 << p.rows.log2_page, C::BN);
+    const int boxes = C::BN / page_rows;                    // pages (or parts of one) a tile: at most 16
+    const int out_row = p.rows.num_pages << p.rows.log2_page;   // past the cache: TMA fills zeros
+    // cache row of the page's part that lane l loads of tile i
+    auto box_row = [&](int i) -> int {
+      const int j = kbeg + i * C::BN + lane * page_rows;
+      if (lane >= boxes || i >= n || j >= end) return out_row;
+      const long long row = p.rows.row(b, j);
+      if (row < 0) {
+        atomicOr(p.status, kStBadPage);
+        return out_row;
+      }
+      return static_cast<int>(row);
+    };
+    int use = 0;
+    bool ok = true;
+    // the next slot of the ring, empty, its barrier told of a tile; -1: given up
+    auto slot = [&](uint32_t bar_of_tail) -> int {
+      const int s = use % C::NST, u = use / C::NST;
+      if (u > 0) {
+        ok = ok && mbar_wait(empty_bar(s), (u - 1) & 1, abort_flag, p.status, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) return -1;
+      if (lane == 0) mbar_arrive_expect_tx(bar_of_tail ? bar_of_tail : full_bar(s), C::TILE);
+      __syncwarp();
+      ++use;
+      return s;
+    };
+    auto load = [&](const CUtensorMap* tm, int s, uint32_t bar, int row) {
+      if (lane < boxes) {
+#pragma unroll
+        for (int a = 0; a < C::ATOMS; ++a)
+          tma_load_3d(ring + s * C::TILE + a * C::ATOM + lane * page_rows * 128, tm, bar, a * 64, hk, row);
+      }
+    };
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    bool tail_used = false;
+    int next = box_row(0);
+    for (int i = 0; i < n; ++i) {
+      const int row = next;
+      next = box_row(i + 1);
+      int s = slot(0);
+      if (s < 0) break;
+      load(&tm_k, s, full_bar(s), row);
+      // the last tile's rows behind the last key that anyone sees may hold
+      // anything (0 * NaN is not 0): its values are landed here, zeroed there,
+      // and only then handed on
+      const int valid = end - (kbeg + i * C::BN);
+      if (valid >= C::BN) {
+        s = slot(0);
+        if (s < 0) break;
+        load(&tm_v, s, full_bar(s), row);
+      } else {
+        s = slot(tail_bar);
+        if (s < 0) break;
+        load(&tm_v, s, tail_bar, row);
+        tail_used = true;
+        ok = mbar_wait(tail_bar, 0, abort_flag, p.status, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        uint8_t* at = smem + C::OFF_RING + s * C::TILE;
+        for (int x = valid * 8 + lane; x < C::BN * 8; x += 32) {
+#pragma unroll
+          for (int a = 0; a < C::ATOMS; ++a)
+            *reinterpret_cast<uint4*>(at + a * C::ATOM + x * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_bar(s));
+        if (!ok) break;
+      }
+    }
+    // never leave the CTA with a copy still landing in its shared memory
+    if (tail_used) mbar_wait_cleanup(tail_bar, 0);
+    for (int u = max(0, use - C::NST); u < use; ++u) mbar_wait_cleanup(full_bar(u % C::NST), (u / C::NST) & 1);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16(C::BM, C::BN);
+      constexpr uint32_t idesc_o = umma_idesc_bf16(C::BM, D) | kIdescBNMajor;
+      bool ok = mbar_wait(q_bar, 0, abort_flag, p.status, p.wait_ns);
+      auto landed = [&](int u) {
+        ok = ok && mbar_wait(full_bar(u % C::NST), (u / C::NST) & 1, abort_flag, p.status, p.wait_ns);
+      };
+      auto scores = [&](int t, int u) {
+        const uint32_t sq = sbase + C::OFF_Q + t * C::TILE, sk = ring + (u % C::NST) * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::ATOM + (kk & 3) * 32;
+          umma_bf16(tmem + C::S_COL + t * C::BN, sw128_kmajor_desc(sq + off), sw128_kmajor_desc(sk + off), idesc_s,
+                    kk > 0 ? 1u : 0u);
+        }
+        umma_commit(s_bar(t));
+      };
+      // ring uses: key tile i is use 2 i, value tile i use 2 i + 1
+      landed(0);
+      tc_fence_after();
+      if (ok) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (nk[t] > 0) scores(t, 0);
+        umma_commit(empty_bar(0));
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        landed(2 * i + 1);
+        if (i + 1 < n) landed(2 * i + 2);
+        if (!ok) break;
+        const uint32_t sv = ring + ((2 * i + 1) % C::NST) * C::TILE;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (i >= nk[t]) continue;
+          ok = ok && mbar_wait(p_bar(t), i & 1, abort_flag, p.status, p.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < C::BN / 16; ++kk)
+            umma_bf16_ts(tmem + C::O_COL + t * D, tmem + C::S_COL + t * C::BN + kk * 8,
+                         sw128_nmajor_desc(sv + kk * 2048, C::ATOM), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+          if (i + 1 < nk[t])
+            scores(t, 2 * i + 2);
+          else
+            umma_commit(o_bar(t));
+        }
+        if (!ok) break;
+        umma_commit(empty_bar((2 * i + 1) % C::NST));
+        if (i + 1 < n) umma_commit(empty_bar((2 * i + 2) % C::NST));
+      }
+      // all products must be complete before TMEM is given back
+      umma_commit(done_bar);
+      mbar_wait_cleanup(done_bar, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int tid = threadIdx.x - 64;
+    const int t = tid >> 7;
+    const int r = (warp & 3) * 32 + lane;                   // row of the tile = TMEM lane
+    // both query tiles into shared memory, 16 bytes a thread a step, in the swizzled layout
+    constexpr int CH = D / 8;
+    for (int x = tid; x < 2 * C::BM * CH; x += 256) {
+      const int row = x / CH, ch = x % CH;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r0 + row < total) {
+        const int tok = sp.tok0 + (r0 + row) / p.grp, h = hk * p.grp + (r0 + row) % p.grp;
+        v = *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(tok) * p.Hq + h) * D + ch * 8);
+      }
+      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (ch >> 3) * C::ATOM + (row & 127) * 128 +
+                                (((ch & 7) ^ (row & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(q_bar);
+
+    const int pr = r0 + t * C::BM + r;                      // packed row
+    const bool row_ok = pr < total;
+    const int lim = lim_of(min(pr, total - 1));
+    // the warp's first row sees the fewest keys (rows behind the last are zeros and go nowhere)
+    const int wlim = lim_of(min(r0 + t * C::BM + (warp & 3) * 32, total - 1));
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lane_base + C::S_COL + t * C::BN;
+    const uint32_t to = tmem + lane_base + C::O_COL + t * D;
+    float m = neg_inf(), l = 0.f;                           // reference maximum (raw scores), sum
+    bool ok = true;
+    const int mine = t == 0 ? nk[0] : nk[1];
+    for (int i = 0; i < mine; ++i) {
+      ok = mbar_wait(s_bar(t), i & 1, abort_flag, p.status, p.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      uint32_t s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, s + 32 * c);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 128; ++c) reg_fence(s[c]);
+      const int j0 = kbeg + i * C::BN;
+      if (j0 + C::BN > wlim) {
+        const int seen = lim - j0;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= seen) s[c] = 0xff800000u;
+      }
+      float mx4[4] = {m, m, m, m};
+#pragma unroll
+      for (int c = 0; c < 128; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      if (i == 0) {
+        m = mx;
+      } else if (__any_sync(0xffffffffu, (mx - m) * p.scale_log2 > kRescaleLog2)) {
+        const float f = mx == neg_inf() ? 1.f : fast_exp2((m - mx) * p.scale_log2);
+        m = mx;
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(to + 32 * c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            reg_fence(o[x]);
+            o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+          }
+          tmem_st_32x32b_x32(to + 32 * c, o);
+        }
+      }
+      const float off = m == neg_inf() ? 0.f : -m * p.scale_log2;
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float a = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * c]), p.scale_log2, off));
+          const float e = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * c + 1]), p.scale_log2, off));
+          l4[c & 1] += a;
+          l4[2 + (c & 1)] += e;
+          w[c] = pack_bf16(a, e);
+        }
+        tmem_st_32x32b_x32(ts + 32 * h, w);
+      }
+      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(p_bar(t));
+    }
+    if (ok && mine > 0) ok = mbar_wait(o_bar(t), 0, abort_flag, p.status, p.wait_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok) {
+      tc_fence_after();
+      const float inv = mine > 0 && l != 0.f ? 1.f / l : 0.f;
+      const float lse2 = mine > 0 && l != 0.f ? fmaf(m, p.scale_log2, log2f(l)) : neg_inf();
+      const long long row = row_ok ? (static_cast<long long>(sp.tok0) + pr / p.grp) * p.Hq + hk * p.grp + pr % p.grp : 0;
+      const long long at = static_cast<long long>(split) * p.rows.T * p.Hq + row;
+      bool fine = true;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (mine > 0) {
+          tmem_ld_32x32b_x32(to + 32 * c, o);
+          tmem_ld_wait();
+        }
+        float f[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          if (mine > 0) reg_fence(o[x]);
+          f[x] = mine > 0 ? __uint_as_float(o[x]) * inv : 0.f;
+          fine = fine && fabsf(f[x]) < __int_as_float(0x7f800000);
+        }
+        if (!row_ok) continue;
+        if (p.nsplit > 1) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 4)
+            *reinterpret_cast<float4*>(p.part_o + at * D + 32 * c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) store8_bf16(p.out + row * D + 32 * c + x, f + x);
+        }
+      }
+      if (row_ok) {
+        if (p.nsplit > 1)
+          p.part_lse[at] = lse2;
+        else if (p.lse)
+          p.lse[row] = lse2 * kLn2;
+      }
+      // rows with a value that is not finite, one by one over the keys that they see alone
+      for (unsigned todo = __ballot_sync(0xffffffffu, row_ok && !fine); todo; todo &= todo - 1) {
+        const int x = __ffs(todo) - 1;
+        const long long rx = __shfl_sync(0xffffffffu, row, x);
+        const int lx = __shfl_sync(0xffffffffu, lim, x);
+        float o[D / 32], z;
+        attend_row_exact<D>(p, b, hk, rx, kbeg, min(lx, kbeg + chunk), lane, o, &z);
+        if (p.nsplit > 1) {
+          const long long ax = static_cast<long long>(split) * p.rows.T * p.Hq + rx;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) p.part_o[ax * D + lane * (D / 32) + c] = o[c];
+          if (lane == 0) p.part_lse[ax] = z;
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 32; c += 2)
+            *reinterpret_cast<uint32_t*>(p.out + rx * D + lane * (D / 32) + c) = pack_bf16(o[c], o[c + 1]);
+          if (lane == 0 && p.lse) p.lse[rx] = z * kLn2;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace pivot

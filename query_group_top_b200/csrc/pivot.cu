@@ -27,7 +27,7 @@
 #include "../../include/pivot.h"
 #include "attend.cuh"
 #include "finalize.cuh"
-#include "paged_attend.cuh"
+#include "paged_attend_tc.cuh"
 #include "proxy_decode.cuh"
 #include "ptx.cuh"
 #include "refine.cuh"

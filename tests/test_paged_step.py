@@ -100,8 +100,8 @@ def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 64, 1, 1, 1, 1, 0, ptr, None) == 1
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 32, 1, 1, 1, 1, 1, ptr, None) == 2
     # the workspace is host arithmetic: parts of a long axis for few rows, none where the rows fill the device
-    assert lib.pivot_paged_attention_workspace_size(2, 1, 16, 16, 128, 131072) >= 2 * 2 * 16 * 129 * 4
-    assert lib.pivot_paged_attention_workspace_size(0, 1, 16, 16, 128, 131072) == 0
+    assert lib.pivot_paged_attention_workspace_size(2, 1, 16, 16, 128, 16, 131072) >= 2 * 2 * 16 * 129 * 4
+    assert lib.pivot_paged_attention_workspace_size(0, 1, 16, 16, 128, 16, 131072) == 0
 
 
 @pytest.fixture(scope="module")
@@ -380,6 +380,10 @@ ATTEND = [  # held, new, Hq, Hk, d, page, itself, ragged
     ([1000], [200], 8, 1, 128, 16, True, True),
     ([0], [300], 2, 2, 64, 256, True, True),
     ([2500, 900], [1, 1], 16, 2, 128, 4, True, False),             # split along the keys, tiny pages
+    ([0], [600], 4, 4, 128, 64, True, False),                      # several row tiles, causal inside one key tile
+    ([40, 1], [256, 3], 3, 1, 64, 16, False, True),
+    ([1500], [37], 8, 1, 128, 32, True, True),                     # matrix tiles, split along the keys
+    ([5000, 0], [50, 33], 8, 2, 64, 512, True, True),
     ([127, 128, 129, 255, 256, 257], [1] * 6, 2, 1, 128, 128, True, True),
     ([90], [40], 5, 1, 64, 2, True, True),
     (list(range(0, 80, 2)), [1 + i % 2 for i in range(40)], 2, 2, 64, 16, True, True),
