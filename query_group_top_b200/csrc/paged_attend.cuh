@@ -102,7 +102,7 @@ __device__ __forceinline__ int locate_tile(const PagedRows& p, int grp, int rows
 // a value that is not finite: there a masked position's infinity or NaN may
 // have come in as 0 * inf, and here it does not.
 template <int D>
-__device__ __noinline__ void attend_row_exact(const PagedAttendParams& p, int b, int hk, long long qrow, int j0,
+__device__ __forceinline__ void attend_row_exact(const PagedAttendParams& p, int b, int hk, long long qrow, int j0,
                                               int j1, int lane, float (&o)[D / 32], float* lse2) {
   constexpr int C = D / 32;
   float q[C], m = neg_inf(), l = 0.f;

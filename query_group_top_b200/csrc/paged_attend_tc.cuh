@@ -11,7 +11,7 @@
 //   warp 1      TMEM allocator and MMA issuer (one elected thread):
 //               S_t = Q_t K^T (128 x 128 x d), O_t += P_t V (128 x d x 128),
 //               P_t read from TMEM, V as it lies (keys in rows: N-major)
-//   warps 2-5, 6-9  softmax of tile 0 and tile 1: thread = row.  128 scores in
+//   warps 4-7, 8-11  softmax of tile 0 and tile 1: thread = row.  128 scores in
 //               registers, so maximum and sum need no exchange; P_t goes back to
 //               TMEM in bf16 over the scores it came from
 // While one tile's softmax runs, the tensor cores work for the other.  TMEM:
@@ -41,8 +41,11 @@ struct TcCfg {
   static constexpr int OFF_RING = 2 * TILE;
   static constexpr int OFF_BAR = OFF_RING + NST * TILE;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;      // barriers, alignment slack
-  static constexpr int THREADS = 64 + 256;
+  static constexpr int THREADS = 128 + 256;               // three warpgroups, two warps of the first idle
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // + t * 128, + t * D
+  // registers a thread: 168 at launch, moved from the first warpgroup to the softmax ones, which hold 128 scores
+  static constexpr int REGS_FEW = 72, REGS_MANY = 216;
+  static_assert(REGS_FEW + 2 * REGS_MANY <= 3 * 168, "register shares");
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(SMEM > 116 * 1024, "one CTA an SM: each takes the whole TMEM");
 };
@@ -132,6 +135,10 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // the shares move inside each side's branch: ahead of it, the whole of both sides gets the smaller one
+  if (warp < 4) {
+    regs_dec<C::REGS_FEW>();
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int end = max(kend[0], kend[1]);
@@ -269,9 +276,10 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       umma_commit(done_bar);
       mbar_wait_cleanup(done_bar, 0);
     }
-  } else {
+  } else if (warp >= 4) {
+    regs_inc<C::REGS_MANY>();
     // ------------------------------------------------------------ softmax
-    const int tid = threadIdx.x - 64;
+    const int tid = threadIdx.x - 128;
     const int t = tid >> 7;
     const int r = (warp & 3) * 32 + lane;                   // row of the tile = TMEM lane
     // both query tiles into shared memory, 16 bytes a thread a step, in the swizzled layout
@@ -319,8 +327,9 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       float mx4[4] = {m, m, m, m};
 #pragma unroll
-      for (int c = 0; c < 128; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      for (int c = 0; c < 128; c += 2)
+        mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+      const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
       if (i == 0) {
         m = mx;
       } else if (__any_sync(0xffffffffu, (mx - m) * p.scale_log2 > kRescaleLog2)) {
@@ -341,21 +350,26 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
       }
       const float off = m == neg_inf() ? 0.f : -m * p.scale_log2;
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2), off2 = pair_f32(off, off);
+      uint64_t l2[2] = {0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          const float a = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * c]), p.scale_log2, off));
-          const float e = fast_exp2(fmaf(__uint_as_float(s[64 * h + 2 * c + 1]), p.scale_log2, off));
-          l4[c & 1] += a;
-          l4[2 + (c & 1)] += e;
+          const uint64_t x = pair_f32(__uint_as_float(s[64 * h + 2 * c]), __uint_as_float(s[64 * h + 2 * c + 1]));
+          float a, e;
+          unpair_f32(fma2(x, scale2, off2), a, e);
+          a = fast_exp2(a);
+          e = fast_exp2(e);
+          l2[c & 1] = add2(l2[c & 1], pair_f32(a, e));
           w[c] = pack_bf16(a, e);
         }
         tmem_st_32x32b_x32(ts + 32 * h, w);
       }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      float la, lb;
+      unpair_f32(add2(l2[0], l2[1]), la, lb);
+      l += la + lb;
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(p_bar(t));
