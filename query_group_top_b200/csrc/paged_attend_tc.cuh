@@ -51,6 +51,32 @@ struct TcCfg {
 };
 
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kPolyOf16 = 0;   // of 16 pairs of weights, how many exp2_poly makes
+constexpr int kEarly = 3;      // quarters of a weight tile that are handed on ahead of the rest
+
+// 2^x of two values in fp32 by arithmetic alone (no special-function unit):
+// x = n + f with n whole and |f| <= 1/2, 2^f by its minimax polynomial of
+// degree 5 (fitted here by the Remez exchange; relative error 7.5e-8, with the
+// fp32 roundings below 2.2e-7), and n added to the exponent.  x below -127
+// gives 0 (a subnormal), x must not be NaN.
+__device__ __forceinline__ void exp2_poly(float xa, float xb, float& a, float& b) {
+  const float kMagic = 12582912.f;   // 1.5 2^23: adding it rounds to a whole number in the low bits
+  const uint64_t magic = pair_f32(kMagic, kMagic), unmagic = pair_f32(-kMagic, -kMagic);
+  const uint64_t x = pair_f32(fmaxf(xa, -127.f), fmaxf(xb, -127.f));
+  const uint64_t n = add2(x, magic);
+  const uint64_t f = fma2(add2(n, unmagic), pair_f32(-1.f, -1.f), x);
+  uint64_t r = pair_f32(0x1.5c08e6p-10f, 0x1.5c08e6p-10f);
+  r = fma2(r, f, pair_f32(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
+  r = fma2(r, f, pair_f32(0x1.c6b6e4p-5f, 0x1.c6b6e4p-5f));
+  r = fma2(r, f, pair_f32(0x1.ebf918p-3f, 0x1.ebf918p-3f));
+  r = fma2(r, f, pair_f32(0x1.62e428p-1f, 0x1.62e428p-1f));
+  r = fma2(r, f, pair_f32(0x1.000002p+0f, 0x1.000002p+0f));
+  float na, nb, ra, rb;
+  unpair_f32(n, na, nb);
+  unpair_f32(r, ra, rb);
+  a = __uint_as_float((__float_as_uint(na) << 23) + __float_as_uint(ra));
+  b = __uint_as_float((__float_as_uint(nb) << 23) + __float_as_uint(rb));
+}
 
 template <int D>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
@@ -67,16 +93,17 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   constexpr int B0 = 2 * C::NST;
   const uint32_t q_bar = bar0 + 8u * B0;
   auto s_bar = [&](int t) { return bar0 + 8u * (B0 + 1 + t); };    // scores of tile t are in TMEM
-  auto p_bar = [&](int t) { return bar0 + 8u * (B0 + 3 + t); };    // weights of tile t are in TMEM
-  auto o_bar = [&](int t) { return bar0 + 8u * (B0 + 5 + t); };    // the last product of tile t is done
-  const uint32_t tail_bar = bar0 + 8u * (B0 + 7);
-  const uint32_t done_bar = bar0 + 8u * (B0 + 8);
-  static_assert(8 * (2 * C::NST + 9) <= 224, "barriers");
+  auto p_bar = [&](int t) { return bar0 + 8u * (B0 + 3 + t); };    // the early weights of tile t are in TMEM
+  auto w_bar = [&](int t) { return bar0 + 8u * (B0 + 5 + t); };    // ... the rest of them
+  auto o_bar = [&](int t) { return bar0 + 8u * (B0 + 7 + t); };    // the last product of tile t is done
+  const uint32_t tail_bar = bar0 + 8u * (B0 + 9);
+  const uint32_t done_bar = bar0 + 8u * (B0 + 10);
+  static_assert(8 * (2 * C::NST + 11) <= 224, "barriers");
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 224);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 228);
   int* seq_s = reinterpret_cast<int*>(smem + C::OFF_BAR + 232);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // key heads innermost (neighbouring CTAs share pages), the longest row tiles first
   const long long bid = blockIdx.x;
   const int hk = static_cast<int>(bid % p.Hk);
@@ -95,7 +122,8 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       mbar_init(q_bar, 256);
       for (int t = 0; t < 2; ++t) {
         mbar_init(s_bar(t), 1);
-        mbar_init(p_bar(t), 128);
+        mbar_init(p_bar(t), 4);
+        mbar_init(w_bar(t), 4);
         mbar_init(o_bar(t), 1);
       }
       mbar_init(tail_bar, 1);
@@ -222,58 +250,96 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     for (int u = max(0, use - C::NST); u < use; ++u) mbar_wait_cleanup(full_bar(u % C::NST), (u / C::NST) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n > 0) {
+    // The whole warp walks the loop and one lane issues: a loop of one lane
+    // would move every descriptor from vector to uniform registers, which took
+    // longer than the products (73 cycles an instruction for 64 of work).
+    if (n > 0) {
       constexpr uint32_t idesc_s = umma_idesc_bf16(C::BM, C::BN);
       constexpr uint32_t idesc_o = umma_idesc_bf16(C::BM, D) | kIdescBNMajor;
-      bool ok = mbar_wait(q_bar, 0, abort_flag, p.status, p.wait_ns);
-      auto landed = [&](int u) {
-        ok = ok && mbar_wait(full_bar(u % C::NST), (u / C::NST) & 1, abort_flag, p.status, p.wait_ns);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int nu = __shfl_sync(0xffffffffu, n, 0);
+      const int n0 = __shfl_sync(0xffffffffu, nk[0], 0), n1 = __shfl_sync(0xffffffffu, nk[1], 0);
+      const uint64_t qd = sw128_kmajor_desc(sbase + C::OFF_Q), kd = sw128_kmajor_desc(ring);
+      const uint64_t vd = sw128_nmajor_desc(ring, C::ATOM);
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns)) != 0;
       };
-      auto scores = [&](int t, int u) {
-        const uint32_t sq = sbase + C::OFF_Q + t * C::TILE, sk = ring + (u % C::NST) * C::TILE;
+      // slot and phase of the ring's next tile (key tile i, then value tile i, ...)
+      int slot = 0;
+      uint32_t phase = 0;
+      auto advance = [&]() {
+        if (++slot == C::NST) slot = 0, phase ^= 1;
+      };
+      auto scores = [&](int t, int ks) {
+        const uint64_t a = qd + static_cast<uint64_t>(t * (C::TILE >> 4)), b_ = kd + static_cast<uint64_t>(ks * (C::TILE >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::ATOM + (kk & 3) * 32;
-          umma_bf16(tmem + C::S_COL + t * C::BN, sw128_kmajor_desc(sq + off), sw128_kmajor_desc(sk + off), idesc_s,
-                    kk > 0 ? 1u : 0u);
+          const uint64_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
+          umma_bf16(tm + C::S_COL + t * C::BN, a + off, b_ + off, idesc_s, kk > 0 ? 1u : 0u);
         }
         umma_commit(s_bar(t));
       };
-      // ring uses: key tile i is use 2 i, value tile i use 2 i + 1
-      landed(0);
-      tc_fence_after();
+      auto products = [&](int t, int vs, int k0, int k1, bool first) {
+        const uint64_t b_ = vd + static_cast<uint64_t>(vs * (C::TILE >> 4));
+#pragma unroll
+        for (int kk = k0; kk < k1; ++kk)
+          umma_bf16_ts(tm + C::O_COL + t * D, tm + C::S_COL + t * C::BN + kk * 8, b_ + static_cast<uint64_t>(kk * (2048 >> 4)),
+                       idesc_o, first && kk == 0 ? 0u : 1u);
+      };
+      bool ok = wait(q_bar, 0) && wait(full_bar(0), 0);
       if (ok) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (nk[t] > 0) scores(t, 0);
-        umma_commit(empty_bar(0));
+        tc_fence_after();
+        if (elect_one()) {
+          if (n0 > 0) scores(0, 0);
+          if (n1 > 0) scores(1, 0);
+          umma_commit(empty_bar(0));
+        }
+        __syncwarp();
       }
-      for (int i = 0; i < n && ok; ++i) {
-        landed(2 * i + 1);
-        if (i + 1 < n) landed(2 * i + 2);
-        if (!ok) break;
-        const uint32_t sv = ring + ((2 * i + 1) % C::NST) * C::TILE;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (i >= nk[t]) continue;
-          ok = ok && mbar_wait(p_bar(t), i & 1, abort_flag, p.status, p.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < C::BN / 16; ++kk)
-            umma_bf16_ts(tmem + C::O_COL + t * D, tmem + C::S_COL + t * C::BN + kk * 8,
-                         sw128_nmajor_desc(sv + kk * 2048, C::ATOM), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
-          if (i + 1 < nk[t])
-            scores(t, 2 * i + 2);
-          else
-            umma_commit(o_bar(t));
+      advance();
+      for (int i = 0; i < nu && ok; ++i) {
+        const int vs = slot;
+        ok = wait(full_bar(vs), phase);
+        advance();
+        const int ks = slot;
+        if (i + 1 < nu) {
+          ok = ok && wait(full_bar(ks), phase);
+          advance();
         }
         if (!ok) break;
-        umma_commit(empty_bar((2 * i + 1) % C::NST));
-        if (i + 1 < n) umma_commit(empty_bar((2 * i + 2) % C::NST));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t == 0 ? n0 : n1;
+          if (i >= nt) continue;
+          ok = ok && wait(p_bar(t), i & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (kEarly < 4) {
+            if (elect_one()) products(t, vs, 0, 2 * kEarly, i == 0);
+            __syncwarp();
+            ok = wait(w_bar(t), i & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (elect_one()) {
+            products(t, vs, kEarly < 4 ? 2 * kEarly : 0, 8, i == 0);
+            if (i + 1 < nt)
+              scores(t, ks);
+            else
+              umma_commit(o_bar(t));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          umma_commit(empty_bar(vs));
+          if (i + 1 < nu) umma_commit(empty_bar(ks));
+        }
+        __syncwarp();
       }
       // all products must be complete before TMEM is given back
-      umma_commit(done_bar);
+      if (elect_one()) umma_commit(done_bar);
+      __syncwarp();
       mbar_wait_cleanup(done_bar, 0);
     }
   } else if (warp >= 4) {
@@ -328,11 +394,12 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       float mx4[4] = {m, m, m, m};
 #pragma unroll
       for (int c = 0; c < 128; c += 2)
-        mx4[(c >> 1) & 3] = max3(mx4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
+        mx4[(c >> 1) & 3] = max3_nan(mx4[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+      // NaN where a score is: the reference and with it the whole row then become NaN
+      const float mx = max3_nan(max3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], m);
       if (i == 0) {
         m = mx;
-      } else if (__any_sync(0xffffffffu, (mx - m) * p.scale_log2 > kRescaleLog2)) {
+      } else if (__any_sync(0xffffffffu, !((mx - m) * p.scale_log2 <= kRescaleLog2))) {
         const float f = mx == neg_inf() ? 1.f : fast_exp2((m - mx) * p.scale_log2);
         m = mx;
         l *= f;
@@ -349,30 +416,42 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           tmem_st_32x32b_x32(to + 32 * c, o);
         }
       }
-      const float off = m == neg_inf() ? 0.f : -m * p.scale_log2;
+      // no key seen yet: every weight is 0; an infinite score: every weight is NaN
+      const float off = fabsf(m) < __int_as_float(0x7f800000) ? -m * p.scale_log2 : m == neg_inf() ? 0.f : __int_as_float(0x7fffffff);
       const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2), off2 = pair_f32(off, off);
       uint64_t l2[2] = {0, 0};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
+      for (int h = 0; h < 4; ++h) {
+        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const uint64_t x = pair_f32(__uint_as_float(s[64 * h + 2 * c]), __uint_as_float(s[64 * h + 2 * c + 1]));
+        for (int c = 0; c < 16; ++c) {
+          const uint64_t x = pair_f32(__uint_as_float(s[32 * h + 2 * c]), __uint_as_float(s[32 * h + 2 * c + 1]));
           float a, e;
           unpair_f32(fma2(x, scale2, off2), a, e);
-          a = fast_exp2(a);
-          e = fast_exp2(e);
+          if (c * kPolyOf16 % 16 < kPolyOf16 && kPolyOf16 > 0) {
+            exp2_poly(a, e, a, e);
+          } else {
+            a = fast_exp2(a);
+            e = fast_exp2(e);
+          }
           l2[c & 1] = add2(l2[c & 1], pair_f32(a, e));
           w[c] = pack_bf16(a, e);
         }
-        tmem_st_32x32b_x32(ts + 32 * h, w);
+        tmem_st_32x32b_x16(ts + 16 * h, w);
+        if (h == kEarly - 1) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_bar(t));
+        }
       }
       float la, lb;
       unpair_f32(add2(l2[0], l2[1]), la, lb);
       l += la + lb;
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(p_bar(t));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(w_bar(t));
     }
     if (ok && mine > 0) ok = mbar_wait(o_bar(t), 0, abort_flag, p.status, p.wait_ns);
     ok = __all_sync(0xffffffffu, ok);
