@@ -51,7 +51,12 @@ struct TcCfg {
 };
 
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kPolyOf16 = 0;   // of 16 pairs of weights, how many exp2_poly makes
+// Of 16 pairs of weights, how many exp2_poly makes.  At 64 channels the special
+// functions bound the loop (half the products for as many weights): 3 of 16
+// took 178 us for 197 (4 chunks of 2048 tokens, 16 heads, contexts of 2048);
+// at 128 the products do, and any share is within 1 %.
+template <int D>
+constexpr int kPolyOf16 = D == 64 ? 3 : 0;
 constexpr int kEarly = 3;      // quarters of a weight tile that are handed on ahead of the rest
 
 // 2^x of two values in fp32 by arithmetic alone (no special-function unit):
@@ -348,17 +353,35 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const int tid = threadIdx.x - 128;
     const int t = tid >> 7;
     const int r = (warp & 3) * 32 + lane;                   // row of the tile = TMEM lane
-    // both query tiles into shared memory, 16 bytes a thread a step, in the swizzled layout
-    constexpr int CH = D / 8;
-    for (int x = tid; x < 2 * C::BM * CH; x += 256) {
-      const int row = x / CH, ch = x % CH;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r0 + row < total) {
-        const int tok = sp.tok0 + (r0 + row) / p.grp, h = hk * p.grp + (r0 + row) % p.grp;
-        v = *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(tok) * p.Hq + h) * D + ch * 8);
+    // both query tiles into shared memory in the swizzled layout: a thread takes
+    // one 16-byte piece of every RS-th row (rows behind the last repeat it: they
+    // go nowhere), eight loads in flight
+    constexpr int CH = D / 8, RS = 256 / CH, STEP = 8;
+    {
+      const int ch = tid % CH, row0 = tid / CH;
+      int tok = (r0 + row0) / p.grp, rem = (r0 + row0) % p.grp;   // of the packed row at hand
+      const int dtok = RS / p.grp, drem = RS % p.grp;
+      const int ltok = (total - 1) / p.grp, lrem = p.grp - 1;      // of the last one
+      const uint16_t* qb = p.q + (static_cast<long long>(sp.tok0) * p.Hq + hk * p.grp) * D + ch * 8;
+#pragma unroll
+      for (int x0 = 0; x0 < CH; x0 += STEP) {
+        uint4 v[STEP];
+#pragma unroll
+        for (int y = 0; y < STEP; ++y) {
+          const bool in = tok <= ltok;
+          v[y] = __ldg(reinterpret_cast<const uint4*>(
+              qb + (static_cast<long long>(in ? tok : ltok) * p.Hq + (in ? rem : lrem)) * D));
+          tok += dtok;
+          rem += drem;
+          if (rem >= p.grp) rem -= p.grp, ++tok;
+        }
+#pragma unroll
+        for (int y = 0; y < STEP; ++y) {
+          const int row = row0 + RS * (x0 + y);
+          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (ch >> 3) * C::ATOM + (row & 127) * 128 +
+                                    (((ch & 7) ^ (row & 7)) << 4)) = v[y];
+        }
       }
-      *reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (ch >> 3) * C::ATOM + (row & 127) * 128 +
-                                (((ch & 7) ^ (row & 7)) << 4)) = v;
     }
     fence_proxy_async_smem();
     mbar_arrive(q_bar);
@@ -428,7 +451,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           const uint64_t x = pair_f32(__uint_as_float(s[32 * h + 2 * c]), __uint_as_float(s[32 * h + 2 * c + 1]));
           float a, e;
           unpair_f32(fma2(x, scale2, off2), a, e);
-          if (c * kPolyOf16 % 16 < kPolyOf16 && kPolyOf16 > 0) {
+          if (c * kPolyOf16<D> % 16 < kPolyOf16<D> && kPolyOf16<D> > 0) {
             exp2_poly(a, e, a, e);
           } else {
             a = fast_exp2(a);
