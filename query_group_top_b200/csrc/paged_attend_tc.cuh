@@ -110,7 +110,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // key heads innermost (neighbouring CTAs share pages), the longest row tiles first
-  const long long bid = blockIdx.x;
+  const unsigned bid = blockIdx.x;
   const int hk = static_cast<int>(bid % p.Hk);
   const int split = static_cast<int>(bid / p.Hk % p.nsplit);
   const int flat = p.tiles - 1 - static_cast<int>(bid / p.Hk / p.nsplit);
@@ -158,15 +158,6 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
   const int n = max(nk[0], nk[1]);
   if (n == 0 && split > 0) return;                          // the join reads no part a row has no keys in
-
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
 
   // the shares move inside each side's branch: ahead of it, the whole of both sides gets the smaller one
   if (warp < 4) {
@@ -258,10 +249,15 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // The whole warp walks the loop and one lane issues: a loop of one lane
     // would move every descriptor from vector to uniform registers, which took
     // longer than the products (73 cycles an instruction for 64 of work).
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+    tc_fence_before();
+    named_barrier(1, 32 + 256);                              // its address, to the softmax warps
+    tc_fence_after();
     if (n > 0) {
       constexpr uint32_t idesc_s = umma_idesc_bf16(C::BM, C::BN);
       constexpr uint32_t idesc_o = umma_idesc_bf16(C::BM, D) | kIdescBNMajor;
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_slot, 0);
       const int nu = __shfl_sync(0xffffffffu, n, 0);
       const int n0 = __shfl_sync(0xffffffffu, nk[0], 0), n1 = __shfl_sync(0xffffffffu, nk[1], 0);
       const uint64_t qd = sw128_kmajor_desc(sbase + C::OFF_Q), kd = sw128_kmajor_desc(ring);
@@ -303,15 +299,19 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       }
       advance();
       for (int i = 0; i < nu && ok; ++i) {
+        // the tile's values and the next tile's keys, nearly always landed: both asked in one vote
         const int vs = slot;
-        ok = wait(full_bar(vs), phase);
+        const uint32_t vph = phase;
         advance();
         const int ks = slot;
-        if (i + 1 < nu) {
-          ok = ok && wait(full_bar(ks), phase);
-          advance();
+        const uint32_t kph = phase;
+        const bool more = i + 1 < nu;
+        if (more) advance();
+        const bool v_in = mbar_try_wait(full_bar(vs), vph), k_in = !more || mbar_try_wait(full_bar(ks), kph);
+        if (!__all_sync(0xffffffffu, v_in && k_in)) {
+          ok = wait(full_bar(vs), vph) && (!more || wait(full_bar(ks), kph));
+          if (!ok) break;
         }
-        if (!ok) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int nt = t == 0 ? n0 : n1;
@@ -385,6 +385,9 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     }
     fence_proxy_async_smem();
     mbar_arrive(q_bar);
+    named_barrier(1, 32 + 256);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
 
     const int pr = r0 + t * C::BM + r;                      // packed row
     const bool row_ok = pr < total;
@@ -540,7 +543,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*tmem_slot, 512);
   }
 }
 
