@@ -25,6 +25,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -59,18 +60,11 @@ class PivotError(RuntimeError):
     pass
 
 
-class _Heads(ctypes.Structure):      # pivot_heads_t
-    _fields_ = [("data", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("token_stride", ctypes.c_longlong),
-                ("head_stride", ctypes.c_longlong), ("heads", ctypes.c_int)]
-
-
-class _Rope(ctypes.Structure):       # pivot_rope_t
-    _fields_ = [("freqs", ctypes.c_void_p), ("amplitude", ctypes.c_double), ("eps", ctypes.c_double),
-                ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int)]
-
-
-class _Attend(ctypes.Structure):     # pivot_attend_t
-    _fields_ = [("scale", ctypes.c_double), ("include_self", ctypes.c_int)]
+# The C ABI's option structs, packed: pivot_heads_t (data, weight, token_stride, head_stride, heads), pivot_rope_t
+# (freqs, amplitude, eps, rot_dim, layout), pivot_attend_t (scale, include_self).
+_HEADS = struct.Struct("@PPqqi4x").pack
+_ROPE = struct.Struct("@Pddii").pack
+_ATTEND = struct.Struct("@di4x").pack
 
 
 def library_path() -> str:
@@ -345,107 +339,130 @@ def sparse_attention(q, k, v, idx, cu_seqlens=None, g=1, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ the serving step over a paged cache
+# These calls are short (a decode step's take a few microseconds on the device), so their checks read each
+# attribute of a tensor once and build what the C call takes from it.
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _NOTHING = contextlib.nullcontext()
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)     # the same, without a Stream object
 
 
 def _where(device, stream, tensors):
     """(raw stream, context) of a call on `device`: the given stream, or the device's current one, with the device
     made current.  What the call allocates belongs to that stream; inputs that were made on another one are marked
     as used by it, so that freeing them does not hand their memory out under the call."""
+    index = device.index
     if stream is None:
-        s = torch.cuda.current_stream(device)
-        ctx = _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        return s.cuda_stream, ctx
+        return _raw_stream(index), _NOTHING if index == torch.cuda.current_device() else torch.cuda.device(device)
     if stream.device != device:
         raise PivotError(f"the stream is of {stream.device}, the tensors are on {device}")
-    if stream != torch.cuda.current_stream(device):
+    raw = stream.cuda_stream
+    if raw != _raw_stream(index):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    return raw, torch.cuda.stream(stream)
 
 
-def _on_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise PivotError(f"{name} must be on {device} (is on {t.device})")
-
-
-def _tokens(name, x, g_shape=None):
-    """(leading shape, heads, d) of new tokens' rows x: [T, H, d], or [B, g, H, d]."""
+def _tokens(name, x):
+    """(leading shape, heads, d, device) of new tokens' rows x: [T, H, d], or [B, g, H, d]."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise PivotError(f"{name} must be a CUDA tensor")
-    if x.dim() not in (3, 4):
+    sh = x.shape
+    if not 3 <= len(sh) <= 4:
         raise PivotError(f"{name} must be [T, heads, d] or [B, g, heads, d]")
-    return tuple(x.shape[:-2]), x.shape[-2], x.shape[-1]
+    d = sh[-1]
+    if d != 64 and d != 128:
+        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
+    return sh[:-2], sh[-2], d, x.device
 
 
-def _heads(name, x, weight, lead, d, dtype):
+def _heads(name, x, weight, lead, d, dtype, device):
     """pivot_heads_t of x [*lead, heads, d], which may be a strided view (a slice of a fused projection)."""
     if x is None:
         if weight is not None:
             raise PivotError(f"a norm weight without {name}")
         return None
-    got, H, dx = _tokens(name, x)
-    if got != lead or dx != d:
-        raise PivotError(f"{name} must be {[*lead]} tokens of heads of {d} channels (got {[*x.shape]})")
-    if x.dtype != dtype or dtype not in _DTYPES:
-        raise PivotError(f"{name} must be bfloat16, float16 or float32, and the call's tensors of one type (got {x.dtype})")
-    st = x.stride()
-    if st[-1] != 1:
-        raise PivotError(f"{name}'s channels must be adjacent")
-    ts = st[-3]
-    if x.dim() == 4:
-        if x.shape[1] == 1:
-            ts = st[0]
-        elif x.shape[0] > 1 and st[0] != x.shape[1] * st[1]:
-            raise PivotError(f"{name}'s tokens must be evenly spaced (strides {st})")
-    if x.numel() == d * H:
-        ts = 0
-    hs = st[-2] if H > 1 else 0
+    sh = x.shape
+    if sh[:-2] != lead or sh[-1] != d:
+        raise PivotError(f"{name} must be {[*lead]} tokens of heads of {d} channels (got {[*sh]})")
+    if x.dtype is not dtype or x.device != device:
+        raise PivotError(f"{name} must be {dtype} on {device}, as the call's other tensors (is {x.dtype} on {x.device})")
+    H, ptr = sh[-2], x.data_ptr()
+    if x.is_contiguous():
+        ts, hs = H * d, d
+    else:
+        st = x.stride()
+        if st[-1] != 1:
+            raise PivotError(f"{name}'s channels must be adjacent")
+        ts = st[-3]
+        if len(sh) == 4:
+            if sh[1] == 1:
+                ts = st[0]
+            elif sh[0] > 1 and st[0] != sh[1] * ts:
+                raise PivotError(f"{name}'s tokens must be evenly spaced (strides {st})")
+        if x.numel() == d * H:
+            ts = 0
+        hs = st[-2] if H > 1 else 0
     step = 16 // x.element_size()
-    if x.data_ptr() % 16 or ts % step or hs % step or H < 1:
+    if ptr % 16 or ts % step or hs % step or H < 1:
         raise PivotError(f"{name}'s rows must start on 16-byte boundaries")
+    w = 0
     if weight is not None:
-        if weight.dtype != dtype or tuple(weight.shape) != (d,) or not weight.is_contiguous() or weight.device != x.device \
-                or weight.data_ptr() % 16:
-            raise PivotError(f"{name}_weight must be a contiguous, 16-byte aligned {dtype} tensor of {d} channels on {x.device}")
-    return _Heads(x.data_ptr(), _ptr(weight), ts, hs, H)
+        w = weight.data_ptr()
+        if (weight.dtype is not dtype or weight.shape != (d,) or not weight.is_contiguous() or weight.device != device
+                or w % 16):
+            raise PivotError(f"{name}_weight must be a contiguous, 16-byte aligned {dtype} tensor of {d} channels on {device}")
+    return _HEADS(ptr, w, ts, hs, H)
 
 
 def _rope(freqs, layout, amplitude, eps, d, device):
     if layout not in _LAYOUTS:
         raise PivotError('layout must be "half" or "interleaved"')
-    if not (eps >= 0.0 and math.isfinite(eps) and math.isfinite(amplitude)):
+    if not (0.0 <= eps < math.inf and -math.inf < amplitude < math.inf):
         raise PivotError("eps must be >= 0, and eps and amplitude finite")
     if freqs is None:
-        return _Rope(None, 1.0, eps, 0, 0)
-    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous() or freqs.device != device:
+        return _ROPE(0, 1.0, eps, 0, 0)
+    sh = freqs.shape
+    if freqs.dtype is not torch.float64 or len(sh) != 1 or not freqs.is_contiguous() or freqs.device != device:
         raise PivotError(f"freqs must be a contiguous float64 vector of rot_dim / 2 frequencies on {device}")
-    rot = 2 * freqs.numel()
+    rot = 2 * sh[0]
     if rot < 16 or rot > d or rot % 16:
         raise PivotError(f"rot_dim must be a multiple of 16 in [16, d] (got {rot})")
-    return _Rope(freqs.data_ptr(), amplitude, eps, rot, _LAYOUTS[layout])
+    return _ROPE(freqs.data_ptr(), amplitude, eps, rot, _LAYOUTS[layout])
 
 
 def _int32(name, t, device, shape):
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or not t.is_contiguous()
-            or (tuple(t.shape) != shape)):
-        raise PivotError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or t.device != device
+            or not t.is_contiguous()):
+        raise PivotError(f"{name} must be a contiguous int32 tensor of shape {[*shape]} on {device}")
     return t.data_ptr()
 
 
-def _pages(kpages, vpages, block_table, device, d, names=("kpages", "vpages")):
+def _like(out, x, dtype, device, name):
+    """`out` checked, or a new contiguous tensor of x's shape."""
+    if out is not None:
+        return _out(out, x.shape, dtype, device, name)
+    if x.dtype is dtype and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype, device=device)
+
+
+def _pages(kpages, vpages, block_table, device, d):
     """(num_pages, page_size, heads, max_pages) of a paged cache."""
-    for name, t in zip(names, (kpages, vpages)):
-        if t is None:
-            continue
-        _check_bf16(name, t, 4)
-        if t.device != device or t.shape[-1] != d or t.shape != kpages.shape:
-            raise PivotError(f"{name} must be [num_pages, page_size, heads, {d}] on {device}, keys and values alike")
-    n, page, H, _ = kpages.shape
+    sh = kpages.shape
+    for name, t in (("kpages", kpages), ("vpages", vpages)):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.device != device or t.shape != sh or len(sh) != 4
+                              or sh[3] != d or not t.is_contiguous()):
+            raise PivotError(f"{name} must be contiguous bfloat16 [num_pages, page_size, heads, {d}] on {device}, keys "
+                             f"and values alike")
+    n, page, H, _ = sh
     if page < 1 or page & (page - 1):
         raise PivotError(f"page_size must be a power of two (got {page})")
     if n < 1 or H < 1:
@@ -455,19 +472,20 @@ def _pages(kpages, vpages, block_table, device, d, names=("kpages", "vpages")):
     return n, page, H, block_table.shape[1]
 
 
-def _sequences(lead, T, cu, seqlens, block_table, device, cu_name):
-    """(B, g, pointer of cu, of seqlens, of block_table) of a call's new tokens."""
-    B = block_table.shape[0]
+def _sequences(lead, cu, seqlens, block_table, device, cu_name):
+    """(T, B, g, pointer of cu, of seqlens, of block_table) of a call's new tokens."""
+    bt = block_table.shape
+    B = bt[0]
     if cu is None:
         if len(lead) != 2 or lead[0] != B:
             raise PivotError(f"without {cu_name}, the new tokens are [B, g, heads, d] with block_table's B = {B}")
         g, pcu = lead[1], None
+        T = B * g
     else:
         if len(lead) != 1:
             raise PivotError(f"with {cu_name}, the new tokens are [T, heads, d]")
-        g, pcu = 0, _int32(cu_name, cu, device, (B + 1,))
-    return B, g, pcu, _int32("seqlens", seqlens, device, (B,)), _int32("block_table", block_table, device,
-                                                                     tuple(block_table.shape))
+        g, T, pcu = 0, lead[0], _int32(cu_name, cu, device, (B + 1,))
+    return T, B, g, pcu, _int32("seqlens", seqlens, device, (B,)), _int32("block_table", block_table, device, bt)
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=None, beta_fast=32.0,
@@ -520,28 +538,33 @@ def qk_rope(q, k, positions, freqs, layout="half", amplitude=1.0, q_weight=None,
     x = q if q is not None else k
     if x is None:
         raise PivotError("qk_rope needs q or k")
-    lead, _, d = _tokens("q" if q is not None else "k", x)
-    device = x.device
-    _on_device(device, q=q, k=k)
-    if d not in (64, 128):
-        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
-    hq = _heads("q", q, q_weight, lead, d, x.dtype)
-    hk = _heads("k", k, k_weight, lead, d, x.dtype)
+    lead, _, d, device = _tokens("q" if q is not None else "k", x)
+    dtype = x.dtype
+    if dtype not in _DTYPES:
+        raise PivotError(f"q and k must be bfloat16, float16 or float32 (got {dtype})")
+    hq = _heads("q", q, q_weight, lead, d, dtype, device)
+    hk = _heads("k", k, k_weight, lead, d, dtype, device)
     rope = _rope(freqs, layout, amplitude, eps, d, device)
     T = math.prod(lead)
     pos = None
     if freqs is not None:
         if positions is None or positions.numel() != T:
             raise PivotError("positions must hold one int32 position a token")
-        pos = _int32("positions", positions, device, tuple(positions.shape))
+        pos = _int32("positions", positions, device, positions.shape)
     sp, ctx = _where(device, stream, (q, k, positions, freqs, q_weight, k_weight, out_q, out_k))
     with ctx:
-        out_q = _out(out_q, q.shape, torch.bfloat16, device, "out_q") if q is not None else None
-        out_k = _out(out_k, k.shape, torch.bfloat16, device, "out_k") if k is not None else None
+        pq = pk = None
+        if q is not None:
+            out_q = _like(out_q, q, torch.bfloat16, device, "out_q")
+            pq = out_q.data_ptr()
+        if k is not None:
+            out_k = _like(out_k, k, torch.bfloat16, device, "out_k")
+            pk = out_k.data_ptr()
         if T:
-            _err(lib, lib.pivot_qk_rope(None if hq is None else ctypes.byref(hq), None if hk is None else ctypes.byref(hk),
-                                        _DTYPES[x.dtype], pos, ctypes.byref(rope), T, d, _ptr(out_q), _ptr(out_k), sp))
-    return out_q, out_k
+            rc = lib.pivot_qk_rope(hq, hk, _DTYPES[dtype], pos, rope, T, d, pq, pk, sp)
+            if rc:
+                _err(lib, rc)
+    return out_q if q is not None else None, out_k if k is not None else None
 
 
 def paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new=None, freqs=None, layout="half", amplitude=1.0,
@@ -557,33 +580,34 @@ def paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new=None, freqs=
     bf16 (None without q).  Sequences that do not fit their table and pages outside the cache are left out and
     reported by sync_status()."""
     lib = load_library()
-    lead, Hk, d = _tokens("k", k)
-    device = k.device
-    _on_device(device, v=v, q=q)
+    lead, Hk, d, device = _tokens("k", k)
+    dtype = k.dtype
+    if dtype not in _DTYPES:
+        raise PivotError(f"k, v and q must be bfloat16, float16 or float32 (got {dtype})")
     if (v is None) != (vpages is None):
         raise PivotError("v and vpages go together")
-    if q is None and (out_q is not None or q_weight is not None):
-        raise PivotError("out_q and q_weight need q")
-    if d not in (64, 128):
-        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
-    hk = _heads("k", k, k_weight, lead, d, k.dtype)
-    hv = _heads("v", v, None, lead, d, k.dtype)
-    hq = _heads("q", q, q_weight, lead, d, k.dtype)
+    if q is None and out_q is not None:
+        raise PivotError("out_q needs q")
+    hk = _heads("k", k, k_weight, lead, d, dtype, device)
+    hv = _heads("v", v, None, lead, d, dtype, device)
+    hq = _heads("q", q, q_weight, lead, d, dtype, device)
     n, page, H, max_pages = _pages(kpages, vpages, block_table, device, d)
-    if H != Hk or (v is not None and hv.heads != Hk):
+    if H != Hk or (v is not None and v.shape[-2] != Hk):
         raise PivotError(f"k and v must have the cache's {H} heads")
     rope = _rope(freqs, layout, amplitude, eps, d, device)
-    T = math.prod(lead)
-    B, g, pcu, psl, pbt = _sequences(lead, T, cu_new, seqlens, block_table, device, "cu_new")
+    T, B, g, pcu, psl, pbt = _sequences(lead, cu_new, seqlens, block_table, device, "cu_new")
     sp, ctx = _where(device, stream, (k, v, q, kpages, vpages, block_table, seqlens, cu_new, freqs, k_weight, q_weight,
                                       out_q))
     with ctx:
-        out_q = _out(out_q, q.shape, torch.bfloat16, device, "out_q") if q is not None else None
+        pq = None
+        if q is not None:
+            out_q = _like(out_q, q, torch.bfloat16, device, "out_q")
+            pq = out_q.data_ptr()
         if T and B:
-            _err(lib, lib.pivot_paged_append(ctypes.byref(hk), None if hv is None else ctypes.byref(hv),
-                                             None if hq is None else ctypes.byref(hq), _DTYPES[k.dtype],
-                                             ctypes.byref(rope), pbt, psl, pcu, T, B, d, g, n, page, max_pages,
-                                             kpages.data_ptr(), _ptr(vpages), _ptr(out_q), sp))
+            rc = lib.pivot_paged_append(hk, hv, hq, _DTYPES[dtype], rope, pbt, psl, pcu, T, B, d, g, n, page, max_pages,
+                                        kpages.data_ptr(), None if vpages is None else vpages.data_ptr(), pq, sp)
+            if rc:
+                _err(lib, rc)
     return out_q
 
 
@@ -598,29 +622,29 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
     max_seqlen bounds seqlens.  scale: d ** -0.5 by default.  out_lse: float32 [..., Hq], the log of each row's sum.
     Returns bf16 with q's shape."""
     lib = load_library()
-    _check_bf16("q", q, q.dim())
-    lead, Hq, d = _tokens("q", q)
-    device = q.device
-    if d not in (64, 128):
-        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
+    lead, Hq, d, device = _tokens("q", q)
+    if q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise PivotError("q must be a contiguous bfloat16 tensor")
     n, page, Hk, max_pages = _pages(kpages, vpages, block_table, device, d)
     if Hq % Hk or Hq < 1:
         raise PivotError(f"q's heads must be a multiple of the cache's {Hk} (got {Hq})")
-    T = math.prod(lead)
-    B, g, pcu, psl, pbt = _sequences(lead, T, cu_q, seqlens, block_table, device, "cu_q")
+    T, B, g, pcu, psl, pbt = _sequences(lead, cu_q, seqlens, block_table, device, "cu_q")
     max_seqlen = int(max_seqlen)
-    opt = _Attend(d ** -0.5 if scale is None else float(scale), 1 if include_self else 0)
+    opt = _ATTEND(d ** -0.5 if scale is None else scale, 1 if include_self else 0)
     sp, ctx = _where(device, stream, (q, kpages, vpages, block_table, seqlens, cu_q, out, out_lse))
     with ctx:
-        out = _out(out, q.shape, torch.bfloat16, device, "out")
+        out = _like(out, q, torch.bfloat16, device, "out")
+        plse = None
         if out_lse is not None:
-            _out(out_lse, q.shape[:-1], torch.float32, device, "out_lse")
+            plse = _out(out_lse, q.shape[:-1], torch.float32, device, "out_lse").data_ptr()
         if T and B:
             nbytes = lib.pivot_paged_attention_workspace_size(T, B, Hq, Hk, d, page, max_seqlen)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-            _err(lib, lib.pivot_paged_attention(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pcu,
-                                                ctypes.byref(opt), T, B, Hq, Hk, d, g, n, page, max_pages, max_seqlen,
-                                                out.data_ptr(), _ptr(out_lse), _ptr(ws), nbytes, sp))
+            rc = lib.pivot_paged_attention(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pcu, opt, T, B,
+                                           Hq, Hk, d, g, n, page, max_pages, max_seqlen, out.data_ptr(), plse,
+                                           None if ws is None else ws.data_ptr(), nbytes, sp)
+            if rc:
+                _err(lib, rc)
     return out
 
 
@@ -629,25 +653,25 @@ def sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out=Non
     pivot_decode_index_paged), kpages and vpages with q's H heads.  Returns float32 [B, g, H, d].  Indices at or
     beyond seqlens[b] and pages outside the cache are left out and reported by sync_status()."""
     lib = load_library()
-    _check_bf16("q", q, 4)
-    lead, H, d = _tokens("q", q)
-    device = q.device
-    if d not in (64, 128):
-        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
+    lead, H, d, device = _tokens("q", q)
+    if q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise PivotError("q must be a contiguous bfloat16 tensor")
     n, page, Hk, max_pages = _pages(kpages, vpages, block_table, device, d)
     if Hk != H:
         raise PivotError(f"q must have the cache's {Hk} heads (got {H})")
-    B, g, _, psl, pbt = _sequences(lead, lead[0] * lead[1], None, seqlens, block_table, device, "cu_q")
+    T, B, g, _, psl, pbt = _sequences(lead, None, seqlens, block_table, device, "cu_q")
     if not isinstance(idx, torch.Tensor) or idx.dim() != 4:
         raise PivotError("idx must be an int32 tensor [B, g, H, top_k]")
-    pidx = _int32("idx", idx, device, (B, g, H, idx.shape[-1]))
+    top_k = idx.shape[3]
+    pidx = _int32("idx", idx, device, (B, g, H, top_k))
     sp, ctx = _where(device, stream, (q, kpages, vpages, block_table, seqlens, idx, out))
     with ctx:
-        out = _out(out, q.shape, torch.float32, device, "out")
-        if idx.numel():
-            _err(lib, lib.pivot_sparse_attention_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl,
-                                                       pidx, B, H, d, g, n, page, max_pages, idx.shape[-1],
-                                                       out.data_ptr(), sp))
+        out = _like(out, q, torch.float32, device, "out")
+        if T and top_k:
+            rc = lib.pivot_sparse_attention_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pidx, B,
+                                                  H, d, g, n, page, max_pages, top_k, out.data_ptr(), sp)
+            if rc:
+                _err(lib, rc)
         else:
             out.zero_()
     return out

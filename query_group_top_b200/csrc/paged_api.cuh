@@ -14,6 +14,19 @@ int log2_of(int x) {
   return l;
 }
 
+// Opts a kernel into its dynamic shared memory, once per device.
+template <auto Kernel>
+int allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};   // a bit a device
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return PIVOT_OK;
+  CUDA_TRY(cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return PIVOT_OK;
+}
+
 // Heads that rope_kernel reads: 16-byte rows of d channels at strides that keep them aligned.
 int head_rows(const char* name, const pivot_heads_t* h, int dtype, HeadRows* out) {
   *out = HeadRows{};
@@ -127,11 +140,11 @@ int launch_attend(const PagedAttendParams& ap, bool tiles, int box_rows, cudaStr
     const int rows = ap.rows.num_pages << ap.rows.log2_page;
     if (int rc = make_rows_map(&mk, ap.kpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
     if (int rc = make_rows_map(&mv, ap.vpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
-    CUDA_TRY(cudaFuncSetAttribute(attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D>::SMEM));
+    if (int rc = allow_smem<attend_tiles_kernel<D>>(TcCfg<D>::SMEM)) return rc;
     TraceScope tr("attend_tiles", st);
     attend_tiles_kernel<D><<<grid, TcCfg<D>::THREADS, TcCfg<D>::SMEM, st>>>(mk, mv, ap);
   } else {
-    CUDA_TRY(cudaFuncSetAttribute(attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, RowsCfg<D>::SMEM));
+    if (int rc = allow_smem<attend_rows_kernel<D>>(RowsCfg<D>::SMEM)) return rc;
     TraceScope tr("attend_rows", st);
     attend_rows_kernel<D><<<grid, 128, RowsCfg<D>::SMEM, st>>>(ap);
   }

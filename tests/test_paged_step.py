@@ -26,7 +26,7 @@ def lib():
 
 
 def heads(p, n=2, ts=256, hs=128, w=None):
-    return qg._Heads(p, w, ts, hs, n)
+    return qg._HEADS(p, w or 0, ts, hs, n)
 
 
 @pytest.fixture()
@@ -38,12 +38,11 @@ def ptr():
 
 
 def test_rope_arguments_are_refused_on_the_host(lib, ptr):
-    ref_ = ctypes.byref
-    rope = qg._Rope(ptr, 1.0, 1e-6, 128, 0)
+    rope = qg._ROPE(ptr, 1.0, 1e-6, 128, 0)
 
     def call(q=heads(ptr), k=None, dtype=0, pos=ptr, rope=rope, T=4, d=128, oq=ptr, ok=None):
-        return lib.pivot_qk_rope(None if q is None else ref_(q), None if k is None else ref_(k), dtype, pos,
-                                 None if rope is None else ref_(rope), T, d, oq, ok, None)
+        return lib.pivot_qk_rope(q, k, dtype, pos,
+                                 rope, T, d, oq, ok, None)
 
     assert call(q=None) == 1                                            # neither q nor k
     assert call(oq=None) == 1                                           # no output
@@ -58,19 +57,18 @@ def test_rope_arguments_are_refused_on_the_host(lib, ptr):
     assert call(q=heads(ptr, hs=4)) == 1
     assert call(oq=ptr + 8) == 1
     for rot in (8, 24, 144, 0, -16):
-        assert call(rope=qg._Rope(ptr, 1.0, 1e-6, rot, 0)) == 1, rot
-    assert call(rope=qg._Rope(ptr, 1.0, 1e-6, 64, 2)) == 1              # no such layout
+        assert call(rope=qg._ROPE(ptr, 1.0, 1e-6, rot, 0)) == 1, rot
+    assert call(rope=qg._ROPE(ptr, 1.0, 1e-6, 64, 2)) == 1              # no such layout
     assert b"layout" in lib.pivot_last_error()
 
 
 def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
-    ref_ = ctypes.byref
-    rope = qg._Rope(ptr, 1.0, 1e-6, 128, 0)
+    rope = qg._ROPE(ptr, 1.0, 1e-6, 128, 0)
 
     def append(k=heads(ptr), v=heads(ptr), q=None, T=4, B=2, d=128, g=2, n=8, page=16, mp=4, kp=ptr, vp=ptr, bt=ptr,
                sl=ptr, cu=None, oq=None):
-        return lib.pivot_paged_append(None if k is None else ref_(k), None if v is None else ref_(v),
-                                      None if q is None else ref_(q), 0, ref_(rope), bt, sl, cu, T, B, d, g, n, page, mp,
+        return lib.pivot_paged_append(k, v,
+                                      q, 0, rope, bt, sl, cu, T, B, d, g, n, page, mp,
                                       kp, vp, oq, None)
 
     assert append(k=None) == 1
@@ -85,7 +83,7 @@ def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
 
     def attend(q=ptr, kp=ptr, vp=ptr, bt=ptr, sl=ptr, cu=None, opt=None, T=4, B=2, Hq=4, Hk=2, d=128, g=2, n=8, page=16,
                mp=4, ms=64, out=ptr, ws=None, nb=0):
-        return lib.pivot_paged_attention(q, kp, vp, bt, sl, cu, None if opt is None else ref_(opt), T, B, Hq, Hk, d, g,
+        return lib.pivot_paged_attention(q, kp, vp, bt, sl, cu, opt, T, B, Hq, Hk, d, g,
                                          n, page, mp, ms, out, None, ws, nb, None)
 
     assert attend(q=None) == 1 and attend(out=None) == 1 and attend(kp=None) == 1 and attend(vp=None) == 1
@@ -95,7 +93,7 @@ def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
     assert attend(T=3) == 1 and attend(g=0) == 1
     assert attend(ms=0) == 1 and attend(ms=1 << 30) == 1
     for s in (0.0, -1.0, math.nan, math.inf):
-        assert attend(opt=qg._Attend(s, 1)) == 1, s
+        assert attend(opt=qg._ATTEND(s, 1)) == 1, s
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, None, 1, 1, 64, 1, 1, 1, 1, 1, ptr, None) == 1
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 64, 1, 1, 1, 1, 0, ptr, None) == 1
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 32, 1, 1, 1, 1, 1, ptr, None) == 2
