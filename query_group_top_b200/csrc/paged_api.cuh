@@ -59,10 +59,11 @@ int paged_rows(const int32_t* block_table, const int32_t* seqlens, const int32_t
 template <int D, class T>
 int launch_rope(const RopeParams& rp, bool half, int grid, cudaStream_t st) {
   TraceScope tr(rp.kpages ? "paged_append" : "qk_rope", st);
+  const size_t smem = static_cast<size_t>(rp.tokens_per_block) * (rp.rot / 2) * sizeof(float2);
   if (half)
-    rope_kernel<D, true, T><<<grid, kRopeNT, 0, st>>>(rp);
+    rope_kernel<D, true, T><<<grid, kRopeNT, smem, st>>>(rp);
   else
-    rope_kernel<D, false, T><<<grid, kRopeNT, 0, st>>>(rp);
+    rope_kernel<D, false, T><<<grid, kRopeNT, smem, st>>>(rp);
   CUDA_TRY(cudaGetLastError());
   return PIVOT_OK;
 }
@@ -83,11 +84,13 @@ int run_rope(RopeParams rp, int dtype, const pivot_rope_t* rope, int d, cudaStre
   DeviceInfo* dev = nullptr;
   if (int rc = device_info(&dev)) return rc;
   rp.status = dev->status;
-  // A block's groups of d/16 lanes take a head each.  Few tokens: one a block,
-  // for the latency; many: as many as give each group some four heads, so that
-  // the cosines' cost is spread and the loads of one head hide the next.
-  const int heads = rp.q.n + rp.k.n + rp.v.n, groups = kRopeNT / (d / 16);
-  int tb = std::min(kRopeMaxTok, std::max(1, 4 * groups / heads));
+  // Tokens a block: its groups of d/16 lanes are dealt out to them, so that each
+  // group finds some eight rows at its token.  Fewer tokens a block where
+  // there are not enough for two blocks an SM: then latency counts, and a token's
+  // heads go to as many groups as there are.
+  const int most = std::max(rp.q.n, std::max(rp.k.n, rp.v.n)), groups = kRopeNT / (d / 16);
+  int tb = 1;
+  while (tb < 16 && tb < groups && 2 * tb * most <= 8 * groups) tb *= 2;
   while (tb > 1 && (rp.T + tb - 1) / tb < 2 * dev->sms) tb >>= 1;
   rp.tokens_per_block = tb;
   const int grid = (rp.T + tb - 1) / tb;

@@ -11,12 +11,15 @@
 // taken in revolutions in fp64 and reduced there: at position 10^6 an fp32
 // product would be off by 0.03 rad.
 //
-// Bound by memory (each channel read once, written once).  A block takes a few
-// tokens: it first makes their rot/2 cosines and sines in shared memory (once
-// a token, not once a head: the fp64 product and the sine cost as much as
-// turning some ten heads), then d/16 lanes take one head each, 16 channels a
-// lane in 16-byte loads, the pair's two halves in the same lane, so that the
-// only exchange is the norm's sum over those lanes.
+// Bound by memory (each channel read once, written once), and next to it by
+// instructions, so the work of a head row is kept to its loads, stores and
+// paired arithmetic: a block takes a few tokens and makes their rot/2 cosines
+// and sines in shared memory (once a token, not once a head: the fp64 product
+// and the sine cost as much as turning some ten heads).  d/16 lanes then take a
+// head row, 16 channels a lane in 16-byte loads, the pair's two halves in the
+// same lane, so that the only exchange is the norm's sum over those lanes; they
+// stay with their token, whose cosines they hold in registers, and walk its
+// heads, so that the next row's address is one addition away.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -49,7 +52,6 @@ struct RopeParams {
 };
 
 constexpr int kRopeNT = 256;
-constexpr int kRopeMaxTok = 16;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -108,28 +110,52 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, const float* f) {
 
 // T: type of x and the weights; HALF: channel pairs (i, i + rot/2), else (2i, 2i+1).
 template <int D, bool HALF, class T>
-__global__ void __launch_bounds__(kRopeNT) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int LG = D / 16;              // lanes a head
+__global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 4 : 3) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int LG = D / 16;              // lanes a head row
   constexpr int GROUPS = kRopeNT / LG;
-  __shared__ float2 cs[kRopeMaxTok * D / 2];
-  __shared__ int pos_s[kRopeMaxTok];
-  __shared__ long long row_s[kRopeMaxTok];  // cache row of the token; -1: leave the token out
+  extern __shared__ float2 cs[];          // [tokens][rot / 2]
+  __shared__ int pos_s[GROUPS];
+  __shared__ long long row_s[GROUPS];     // cache row of the token; -1: leave the token out
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t0 = blockIdx.x * p.tokens_per_block;
-  const int nt = min(p.tokens_per_block, p.T - t0);
+  const int tb = p.tokens_per_block, gpt = GROUPS / tb;   // groups a token
+  const int t0 = blockIdx.x * tb;
+  const int nt = min(tb, p.T - t0);
   const bool paged = p.kpages != nullptr;
+  const int half = p.rot >> 1;
+  const int sub = threadIdx.x % LG, group = threadIdx.x / LG;
+  const int tok = group / gpt, g = group % gpt;           // the group's token of the block, its place there
+  const bool turns = sub < (p.rot >> 4);
+  const int ca = HALF && turns ? 8 * sub : 16 * sub;      // the lane's two runs of 8 channels
+  const int cb = HALF && turns ? 8 * sub + half : 16 * sub + 8;
+  const long long t = t0 + min(tok, nt - 1);
+
+  // A group walks rows g, g + gpt, ... of the token's queries, then keys, then
+  // values, in rounds that are the same for all lanes of a warp (for the norm's
+  // shuffles); behind a kind's last row it repeats that row and drops the result.
+  // The next row is loaded before the one at hand is worked on.
+  const int rq = (p.q.n + gpt - 1) / gpt, rk = rq + (p.k.n + gpt - 1) / gpt, rounds = rk + (p.v.n + gpt - 1) / gpt;
+  Vec8<T> va, vb;
+  auto load = [&](int x) {
+    const HeadRows& src = x < rq ? p.q : x < rk ? p.k : p.v;
+    const int h = min(g + gpt * (x - (x < rq ? 0 : x < rk ? rq : rk)), src.n - 1);
+    const T* row = static_cast<const T*>(src.x) + t * src.token_stride + h * src.head_stride;
+    va.load(row + ca);
+    vb.load(row + cb);
+  };
+  load(0);   // on its way while the positions and angles are worked out
+  const double freq0 = half ? p.freqs[threadIdx.x % half] : 0.0;
 
   for (int i = warp; i < nt; i += kRopeNT / 32) {
-    const int t = t0 + i;
+    const int ti = t0 + i;
     int pos = 0;
     long long row = 0;
     if (paged) {
-      const int b = find_sequence(p.rows, t, lane);
+      const int b = find_sequence(p.rows, ti, lane);
       const NewSpan s = p.rows.span(b);
       row = -1;
-      if (t >= s.tok0 && t < s.tok0 + s.n) {   // tokens behind the last sequence belong to none
-        pos = s.len - s.n + (t - s.tok0);
+      if (ti >= s.tok0 && ti < s.tok0 + s.n) {   // tokens behind the last sequence belong to none
+        pos = s.len - s.n + (ti - s.tok0);
         if (s.ok) {
           row = p.rows.row(b, pos);
           if (row < 0 && lane == 0) atomicOr(p.status, kStBadPage);
@@ -140,7 +166,7 @@ __global__ void __launch_bounds__(kRopeNT) rope_kernel(const __grid_constant__ R
         atomicOr(p.status, kStBadLen);
       }
     } else if (p.rot) {
-      pos = p.positions[t];
+      pos = p.positions[ti];
     }
     if (lane == 0) {
       pos_s[i] = pos;
@@ -148,10 +174,10 @@ __global__ void __launch_bounds__(kRopeNT) rope_kernel(const __grid_constant__ R
     }
   }
   __syncthreads();
-  const int half = p.rot >> 1;
   for (int x = threadIdx.x; x < nt * half; x += kRopeNT) {
     const int i = x / half, c = x - i * half;
-    double rev = static_cast<double>(pos_s[i]) * (p.freqs[c] * 0.15915494309189533577);  // 1 / (2 pi)
+    const double freq = x < kRopeNT ? freq0 : p.freqs[c];
+    double rev = static_cast<double>(pos_s[i]) * (freq * 0.15915494309189533577);   // 1 / (2 pi)
     rev -= rint(rev);
     float sn, co;
     sincospif(static_cast<float>(2.0 * rev), &sn, &co);
@@ -159,67 +185,79 @@ __global__ void __launch_bounds__(kRopeNT) rope_kernel(const __grid_constant__ R
   }
   __syncthreads();
 
-  const int sub = threadIdx.x % LG;
-  const bool turns = sub < (p.rot >> 4);
-  const int ca = HALF && turns ? 8 * sub : 16 * sub;            // the lane's two runs of 8 channels
-  const int cb = HALF && turns ? 8 * sub + half : 16 * sub + 8;
-  const int heads = p.q.n + p.k.n + p.v.n;
-  // whole lane groups share a job; every lane of a warp runs the same number of rounds, for the shuffles
-  const int jobs = nt * heads;
-  for (int j0 = (threadIdx.x & ~31) / LG; j0 < jobs; j0 += GROUPS) {
-    const int j = j0 + lane / LG;
-    const bool on = j < jobs;
-    const int i = on ? j / heads : 0;
-    const int h = on ? j - i * heads : 0;
-    const int kind = h < p.q.n ? 0 : h < p.q.n + p.k.n ? 1 : 2;
-    const HeadRows& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-    const int hh = kind == 0 ? h : kind == 1 ? h - p.q.n : h - p.q.n - p.k.n;
-    const T* x = static_cast<const T*>(src.x) + (t0 + i) * src.token_stride + hh * src.head_stride;
-    float f[16];
-    {
-      Vec8<T> va, vb;
-      va.load(x + ca);
-      vb.load(x + cb);
-      va.get(f);
-      vb.get(f + 8);
-    }
-    if (p.q.weight != nullptr || p.k.weight != nullptr) {
-      float ss = 0.f;
+  const long long row = tok < nt ? row_s[tok] : -1;
+  uint64_t co2[4] = {}, si2[4] = {};                      // of the lane's 8 pairs, two a register pair
+  if (turns && tok < nt) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) ss = fmaf(f[c], f[c], ss);
+    for (int c = 0; c < 4; ++c) {
+      const float2 x = cs[tok * half + 8 * sub + 2 * c], y = cs[tok * half + 8 * sub + 2 * c + 1];
+      co2[c] = pair_f32(x.x, y.x);
+      si2[c] = pair_f32(x.y, y.y);
+    }
+  }
+  for (int x = 0; x < rounds; ++x) {
+    const int kind = x < rq ? 0 : x < rk ? 1 : 2;
+    const HeadRows& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+    const int h = g + gpt * (x - (kind == 0 ? 0 : kind == 1 ? rq : rk));
+    float f[16];
+    va.get(f);
+    vb.get(f + 8);
+    if (x + 1 < rounds) load(x + 1);
+    // channels in register pairs: those of a lane's a halves, then its b halves
+    uint64_t a[4], b[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      a[c] = HALF ? pair_f32(f[2 * c], f[2 * c + 1]) : pair_f32(f[4 * c], f[4 * c + 2]);
+      b[c] = HALF ? pair_f32(f[8 + 2 * c], f[9 + 2 * c]) : pair_f32(f[4 * c + 1], f[4 * c + 3]);
+    }
+    if (src.weight != nullptr) {
+      const T* w = static_cast<const T*>(src.weight);
+      float gw[16];
+      Vec8<T> wa, wb;
+      wa.load(w + ca);
+      wb.load(w + cb);
+      wa.get(gw);
+      wb.get(gw + 8);
+      uint64_t s2 = mul2(a[0], a[0]);
+#pragma unroll
+      for (int c = 1; c < 4; ++c) s2 = fma2(a[c], a[c], s2);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s2 = fma2(b[c], b[c], s2);
+      float lo, hi;
+      unpair_f32(s2, lo, hi);
+      float ss = lo + hi;
 #pragma unroll
       for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (src.weight != nullptr) {
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const T* w = static_cast<const T*>(src.weight);
-        float g[16];
-        Vec8<T> va, vb;
-        va.load(w + ca);
-        vb.load(w + cb);
-        va.get(g);
-        vb.get(g + 8);
+      const float r = rsqrtf(ss * (1.f / D) + p.eps);
+      const uint64_t r2 = pair_f32(r, r);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) f[c] = f[c] * r * g[c];
+      for (int c = 0; c < 4; ++c) {
+        a[c] = mul2(mul2(a[c], r2), HALF ? pair_f32(gw[2 * c], gw[2 * c + 1]) : pair_f32(gw[4 * c], gw[4 * c + 2]));
+        b[c] = mul2(mul2(b[c], r2), HALF ? pair_f32(gw[8 + 2 * c], gw[9 + 2 * c]) : pair_f32(gw[4 * c + 1], gw[4 * c + 3]));
       }
     }
     if (turns && kind != 2) {
-      const float2* t = cs + i * half + 8 * sub;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const int ia = HALF ? c : 2 * c, ib = HALF ? c + 8 : 2 * c + 1;
-        const float a = f[ia], b = f[ib];
-        f[ia] = a * t[c].x - b * t[c].y;
-        f[ib] = b * t[c].x + a * t[c].y;
+      for (int c = 0; c < 4; ++c) {
+        const uint64_t y = a[c], z = b[c];
+        a[c] = fma2(y, co2[c], mul2(z, si2[c] ^ 0x8000000080000000ull));   // the sines' signs turned
+        b[c] = fma2(y, si2[c], mul2(z, co2[c]));
       }
     }
-    if (!on || row_s[i] < 0) continue;
-    uint16_t* dst;
-    if (kind == 0)
-      dst = p.out_q + (static_cast<long long>(t0 + i) * p.q.n + hh) * D;
-    else if (!paged)
-      dst = p.out_k + (static_cast<long long>(t0 + i) * p.k.n + hh) * D;
-    else
-      dst = (kind == 1 ? p.kpages : p.vpages) + (row_s[i] * src.n + hh) * D;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (HALF) {
+        unpair_f32(a[c], f[2 * c], f[2 * c + 1]);
+        unpair_f32(b[c], f[8 + 2 * c], f[9 + 2 * c]);
+      } else {
+        unpair_f32(a[c], f[4 * c], f[4 * c + 2]);
+        unpair_f32(b[c], f[4 * c + 1], f[4 * c + 3]);
+      }
+    }
+    if (row < 0 || h >= src.n) continue;
+    uint16_t* dst = kind == 0 ? p.out_q + (t * p.q.n + h) * D
+                    : paged   ? (kind == 1 ? p.kpages : p.vpages) + (row * src.n + h) * D
+                              : p.out_k + (t * p.k.n + h) * D;
     store8_bf16(dst + ca, f);
     store8_bf16(dst + cb, f + 8);
   }
