@@ -17,7 +17,6 @@
 // memory.
 #pragma once
 
-#include "paged_rows.cuh"
 #include "ptx.cuh"
 
 namespace pivot {
@@ -31,8 +30,6 @@ struct AttendParams {
   float* out;            // [R][H][d]
   int R, H, g, top_k;
   float scale;           // d^-1/2
-  PagedRows rows;        // paged caches: k and v are [pages][page_size][H][d]
-  int* status;
 };
 
 constexpr int kAttNT = 128;
@@ -50,9 +47,7 @@ __device__ __forceinline__ void attend_merge(float& m, float& l, float (&a)[8], 
   m = mn;
 }
 
-// PAGED: keys and values lie in pages behind a block table; an index beyond its
-// sequence, or whose page is not one of the cache, is left out and reported.
-template <int D, bool PAGED>
+template <int D>
 __global__ void __launch_bounds__(kAttNT) sparse_attention_kernel(AttendParams p) {
   constexpr int LPK = D / 8;          // lanes per key row
   constexpr int KPW = 32 / LPK;       // keys per warp step
@@ -77,9 +72,7 @@ __global__ void __launch_bounds__(kAttNT) sparse_attention_kernel(AttendParams p
       qf[2 * c + 1] = __uint_as_float(w[c] & 0xFFFF0000u) * p.scale;
     }
   }
-  const int seq = PAGED ? r / p.g : 0;
-  const int len = PAGED ? min(p.rows.seqlens[seq], p.rows.max_len) : 0;
-  const long long base = !PAGED && p.cu ? static_cast<long long>(p.cu[r / p.g]) : 0;
+  const long long base = p.cu ? static_cast<long long>(p.cu[r / p.g]) : 0;
   const long long rstride = static_cast<long long>(p.H) * D;
   const uint16_t* kb = p.k + (base * p.H + h) * D + part * 8;
   const uint16_t* vb = p.v + (base * p.H + h) * D + part * 8;
@@ -95,7 +88,6 @@ __global__ void __launch_bounds__(kAttNT) sparse_attention_kernel(AttendParams p
   for (int tw = warp * KPW; tw < p.top_k; tw += STREAMS * U) {
     const int t0 = tw + sub;
     int j[U];
-    long long at[U];   // cache row of j
     uint4 kv[U], vv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -104,19 +96,8 @@ __global__ void __launch_bounds__(kAttNT) sparse_attention_kernel(AttendParams p
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      at[u] = j[u];
-      if (PAGED && j[u] >= 0) {
-        at[u] = j[u] < len ? p.rows.row(seq, j[u]) : -1;
-        if (at[u] < 0) {
-          j[u] = -1;
-          atomicOr(p.status, kStBadPage);
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      kv[u] = j[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(kb + at[u] * rstride)) : make_uint4(0, 0, 0, 0);
-      vv[u] = j[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(vb + at[u] * rstride)) : make_uint4(0, 0, 0, 0);
+      kv[u] = j[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(kb + j[u] * rstride)) : make_uint4(0, 0, 0, 0);
+      vv[u] = j[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(vb + j[u] * rstride)) : make_uint4(0, 0, 0, 0);
     }
     float s[U];
 #pragma unroll

@@ -1,0 +1,191 @@
+// The sparse attention over index rows (attend.cuh) on a paged cache: keys and
+// values behind a block table, the rows of a decode step.
+//
+// Bound by the gathers, 2 * d * 2 bytes an index.  A CTA takes one (query,
+// head); its four warps take the row's indices 16 at a time through the ring of
+// paged_attend.cuh, so that what is on its way does not hang on registers or on
+// the arithmetic.  The index of a
+// step is read two steps before its keys and the page one step before, so
+// neither of the two dependent loads is waited for.
+//
+// The products run as there, keys in the rows and the query in the columns of
+// m16n8k16 tiles.  The query stands in all eight columns, so every lane has the
+// scores of its two keys; for the second product column 0 holds the upper 8
+// bits of each fp32 weight, column 1 the next 8, column 2 the last: one chain of
+// products whose three columns add up to the sum under fp32 weights (exact to
+// 2^-25 of a weight).  The results stay fp32.
+//
+// Where the rows are few, a cluster of CTAs shares one row's indices and merges
+// over distributed shared memory, so no workspace is needed.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "paged_attend.cuh"
+
+namespace pivot {
+
+struct AttendPagedParams {
+  const uint16_t* q;       // [B][g][H][d] bf16
+  const uint16_t* kpages;  // [pages][page_size][H][d]
+  const uint16_t* vpages;
+  const int32_t* idx;      // [B][g][H][top_k]
+  PagedRows rows;
+  float* out;              // [B][g][H][d]
+  int H, g, top_k;
+  int parts;               // CTAs of a cluster, each a part of the row's indices
+  float scale_log2;        // d^-1/2 * log2(e)
+  int* status;
+};
+
+__device__ __forceinline__ float round_bf16(float x) {
+  return __uint_as_float(pack_bf16(x, 0.f) << 16);
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __grid_constant__ AttendPagedParams p) {
+  using R = KvRing<D>;
+  constexpr int KS = D / 16;       // k-steps of q . k, and 16-channel tiles of o
+  constexpr int OS = D + 4;        // floats a row of the merge
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const unsigned rh = blockIdx.x / p.parts;                // query row and head
+  const int rank = static_cast<int>(blockIdx.x % p.parts); // the CTA's rank in its cluster
+  const int h = static_cast<int>(rh % p.H);
+  const int b = static_cast<int>(rh / p.H / p.g);
+  const int len = min(p.rows.seqlens[b], p.rows.max_len);
+  const int chunk = ((p.top_k + p.parts - 1) / p.parts + 15) & ~15;
+  const int tbeg = rank * chunk, tend = min(p.top_k, tbeg + chunk);
+  const int32_t* row = p.idx + static_cast<long long>(rh) * p.top_k;
+  R kv;
+  kv.init(smem, p.kpages, p.vpages, p.H, h, warp, lane);
+
+  const int ntiles = tend > tbeg ? (tend - tbeg + R::KT - 1) / R::KT : 0;
+  const int mine = ntiles > warp ? (ntiles - warp + R::NW - 1) / R::NW : 0;
+  // index of the entry that lanes l and l + 16 take of step `it`, then its cache row (-1: none)
+  auto entry = [&](int it) -> int {
+    const int t = tbeg + (warp + it * R::NW) * R::KT + (lane & 15);
+    return it < mine && t < tend ? __ldg(row + t) : -1;
+  };
+  auto place = [&](int j) -> int {
+    if (j < 0) return -1;
+    const long long at = j < len ? p.rows.row(b, j) : -1;
+    if (at < 0) atomicOr(p.status, kStBadPage);
+    return static_cast<int>(at);
+  };
+  int next = place(entry(0));
+  int next_entry = entry(1);
+  uint32_t there[R::ST];                                   // entries that are there, a bit each, of the steps in flight
+#pragma unroll
+  for (int s = 0; s < R::ST; ++s) there[s] = 0;
+  auto issue = [&](int it) {
+    const int at = next, e = next_entry;
+    next_entry = entry(it + 2);
+#pragma unroll
+    for (int s = 0; s + 1 < R::ST; ++s) there[s] = there[s + 1];
+    there[R::ST - 1] = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
+    if (it < mine && there[R::ST - 1]) kv.issue(it, at);
+    cp_async_commit();
+    next = place(e);
+  };
+#pragma unroll
+  for (int s = 0; s < R::ST - 1; ++s) issue(s);
+
+  const int gr = lane >> 2, gc = lane & 3;
+  uint32_t qb[KS][2];
+  {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(rh) * D) + gc;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      qb[k][0] = src[8 * k];
+      qb[k][1] = src[8 * k + 4];
+    }
+  }
+  float o[KS][4], m = neg_inf(), l = 0.f;                  // m: the whole warp's; l: of the lane's keys
+#pragma unroll
+  for (int n = 0; n < KS; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  for (int it = 0; it < mine; ++it) {
+    issue(it + R::ST - 1);
+    cp_async_wait<R::ST - 1>();
+    __syncwarp();
+    const uint32_t mask = there[0];
+    if (mask == 0) continue;
+    const uint32_t kt = kv.keys(it, smem, warp);
+    float s[4];
+    step_scores<D>(kt, qb, lane, s);
+    const float a = mask >> gr & 1 ? s[0] * p.scale_log2 : neg_inf();
+    const float c = mask >> (gr + 8) & 1 ? s[2] * p.scale_log2 : neg_inf();
+    float x = fmaxf(a, c);
+#pragma unroll
+    for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+    if (x > m) {                                           // the same in every lane
+      const float f = fast_exp2(m - x);
+      m = x;
+      l *= f;
+#pragma unroll
+      for (int n = 0; n < KS; ++n) o[n][0] *= f, o[n][1] *= f, o[n][2] *= f, o[n][3] *= f;
+    }
+    const float z = m == neg_inf() ? 0.f : m;
+    const float wa = fast_exp2(a - z), wc = fast_exp2(c - z);
+    l += wa + wc;
+    const float ha = round_bf16(wa), hc = round_bf16(wc), ma = round_bf16(wa - ha), mc = round_bf16(wc - hc);
+    const uint32_t pa = gc == 0 ? pack_bf16(ha, ma) : gc == 1 ? pack_bf16(wa - ha - ma, 0.f) : 0u;
+    const uint32_t pc = gc == 0 ? pack_bf16(hc, mc) : gc == 1 ? pack_bf16(wc - hc - mc, 0.f) : 0u;
+    step_values<D>(kt + R::HALF, transpose_8x8(pa), transpose_8x8(pc), lane, o);
+    __syncwarp();   // every lane has read the slot that the next step's copies fill
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int y = 4; y < 32; y <<= 1) l += __shfl_xor_sync(0xffffffffu, l, y);
+  __syncthreads();
+  // the warps' parts: [warp][OS], then (m, l) of each; the CTA's behind them
+  float* mo = reinterpret_cast<float*>(smem);
+  float* ml = mo + R::NW * OS;
+  float* co = ml + R::NW * 2;
+#pragma unroll
+  for (int n = 0; n < KS; ++n) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      // columns 0 and 1 are lane gc = 0's, column 2 lane gc = 1's
+      const float lo = __shfl_down_sync(0xffffffffu, o[n][e], 1);
+      if (gc == 0) mo[warp * OS + 16 * n + gr + 4 * e] = (lo + o[n][e + 1]) + o[n][e];
+    }
+  }
+  if (lane == 0) ml[2 * warp] = m, ml[2 * warp + 1] = l;
+  __syncthreads();
+  const int c = threadIdx.x;                               // channel
+  float cm = neg_inf(), cl = 0.f, acc = 0.f;
+  if (c < D) {
+#pragma unroll
+    for (int w = 0; w < R::NW; ++w) cm = fmaxf(cm, ml[2 * w]);
+    const float z = cm == neg_inf() ? 0.f : cm;
+#pragma unroll
+    for (int w = 0; w < R::NW; ++w) {
+      const float f = fast_exp2(ml[2 * w] - z);
+      cl = fmaf(f, ml[2 * w + 1], cl);
+      acc = fmaf(f, mo[w * OS + c], acc);
+    }
+  }
+  if (p.parts > 1) {
+    cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+    if (c < D && rank > 0) {
+      co[c] = acc;
+      if (c == 0) co[D] = cm, co[D + 1] = cl;
+    }
+    cluster.sync();
+    if (c < D && rank == 0) {
+      for (int r = 1; r < p.parts; ++r) {
+        const float* ro = cluster.map_shared_rank(co, r);
+        const float rm = ro[D], n = fmaxf(cm, rm), z = n == neg_inf() ? 0.f : n;
+        const float f = fast_exp2(cm - z), e = fast_exp2(rm - z);
+        cl = fmaf(e, ro[D + 1], cl * f);
+        acc = fmaf(e, ro[c], acc * f);
+        cm = n;
+      }
+    }
+    cluster.sync();   // no CTA leaves while its part is being read
+  }
+  if (c < D && rank == 0) p.out[static_cast<long long>(rh) * D + c] = cl == 0.f ? 0.f : acc / cl;
+}
+
+}  // namespace pivot

@@ -108,6 +108,21 @@ int check_dtype(int dtype) {
   return PIVOT_OK;
 }
 
+// How many parts to cut `units` equal pieces of work of `len` keys into, where
+// the device takes `slots` at a time and a part costs as much as `fixed` keys
+// more: the rounds it takes times a part's length.  A cut that leaves a last
+// round nearly empty costs that round (64 sequences, 8 key heads, 8192 keys in
+// 2 parts: 396 us; in 4: 350).
+int best_parts(long long units, long long slots, long long len, long long fixed, long long most) {
+  most = std::min(most, std::max(1ll, 8 * slots / units));
+  long long best = 1, least = -1;
+  for (long long n = 1; n <= most; ++n) {
+    const long long cost = (units * n + slots - 1) / slots * ((len + n - 1) / n + fixed);
+    if (least < 0 || cost < least) least = cost, best = n;
+  }
+  return static_cast<int>(best);
+}
+
 // Which kernel takes a call of paged attention, and how the key axis is split.
 struct AttendPlan {
   bool tiles;               // attend_tiles_kernel, else attend_rows_kernel
@@ -121,12 +136,17 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int page_size, int m
   const long long rows = static_cast<long long>(T) * (Hq / Hk);
   // TMA lays boxes of 8 rows or more into the swizzled tiles, so smaller pages go to the rows kernel
   a.tiles = rows >= 32ll * B && page_size >= 8;
-  a.rows = a.tiles ? 256 : 16;
+  a.rows = a.tiles ? 256 : rows <= 8ll * B ? 8 : 16;
   a.min_chunk = a.tiles ? 512 : 256;
   const long long ctas = std::max<long long>(B, (rows + a.rows - 1) / a.rows) * Hk;
-  const long long want = a.tiles ? 2ll * sms : 8ll * sms;   // two rounds of one CTA an SM; four of two
-  const long long n = std::max<long long>(1, want / ctas);
-  a.nsplit = static_cast<int>(std::min<long long>(n, (max_seqlen + a.min_chunk - 1) / a.min_chunk));
+  if (a.tiles) {
+    a.nsplit = static_cast<int>(std::min<long long>(std::max<long long>(1, 2ll * sms / ctas),
+                                                    (max_seqlen + a.min_chunk - 1) / a.min_chunk));
+  } else {
+    const int per_sm = d == 128 ? KvRing<128>::PER_SM : KvRing<64>::PER_SM;
+    a.nsplit = best_parts(ctas, static_cast<long long>(per_sm) * sms, max_seqlen, 96,
+                          (max_seqlen + a.min_chunk - 1) / a.min_chunk);
+  }
   if (a.nsplit > 1) {
     const size_t parts = static_cast<size_t>(a.nsplit) * T * Hq;
     a.part_lse = up(parts * d * sizeof(float));
@@ -136,7 +156,7 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int page_size, int m
 }
 
 template <int D>
-int launch_attend(const PagedAttendParams& ap, bool tiles, int box_rows, cudaStream_t st) {
+int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, int box_rows, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<long long>(ap.tiles) * ap.Hk * ap.nsplit);
   if (tiles) {
     CUtensorMap mk, mv;
@@ -147,9 +167,14 @@ int launch_attend(const PagedAttendParams& ap, bool tiles, int box_rows, cudaStr
     TraceScope tr("attend_tiles", st);
     attend_tiles_kernel<D><<<grid, TcCfg<D>::THREADS, TcCfg<D>::SMEM, st>>>(mk, mv, ap);
   } else {
-    if (int rc = allow_smem<attend_rows_kernel<D>>(RowsCfg<D>::SMEM)) return rc;
     TraceScope tr("attend_rows", st);
-    attend_rows_kernel<D><<<grid, 128, RowsCfg<D>::SMEM, st>>>(ap);
+    if (rows_per_cta == 8) {
+      if (int rc = allow_smem<attend_rows_kernel<D, 1>>(KvRing<D>::SMEM)) return rc;
+      attend_rows_kernel<D, 1><<<grid, 128, KvRing<D>::SMEM, st>>>(ap);
+    } else {
+      if (int rc = allow_smem<attend_rows_kernel<D, 2>>(KvRing<D>::SMEM)) return rc;
+      attend_rows_kernel<D, 2><<<grid, 128, KvRing<D>::SMEM, st>>>(ap);
+    }
   }
   CUDA_TRY(cudaGetLastError());
   if (ap.nsplit > 1) {
@@ -158,6 +183,37 @@ int launch_attend(const PagedAttendParams& ap, bool tiles, int box_rows, cudaStr
     attend_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(ap);
   }
   CUDA_TRY(cudaGetLastError());
+  return PIVOT_OK;
+}
+
+template <int D>
+int launch_sparse_paged(AttendPagedParams ap, int B, int sms, cudaStream_t st) {
+  const long long units = static_cast<long long>(B) * ap.g * ap.H, slots = static_cast<long long>(KvRing<D>::PER_SM) * sms;
+  // CTAs that share a row's indices: the cluster of 1, 2, 4 or 8 with the least
+  // rounds times length, a part's fixed cost being some 150 indices, and 100
+  // more for the cluster's two barriers
+  int parts = 1;
+  long long least = -1;
+  for (int n = 1; n <= 8; n *= 2) {
+    const long long cost = (units * n + slots - 1) / slots * ((ap.top_k + n - 1) / n + 150) + (n > 1 ? 100 : 0);
+    if (least < 0 || cost < least) least = cost, parts = n;
+  }
+  if (units * parts >= (1ll << 31)) return fail(PIVOT_ERR_INVALID_ARG, "B * g * H too large");
+  ap.parts = parts;
+  if (int rc = allow_smem<sparse_attention_paged_kernel<D>>(KvRing<D>::SMEM)) return rc;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * parts));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = KvRing<D>::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(parts);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = parts > 1 ? 1 : 0;
+  TraceScope tr("sparse_attention_paged", st);
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, sparse_attention_paged_kernel<D>, ap));
   return PIVOT_OK;
 }
 
@@ -256,7 +312,8 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   ap.wait_ns = wait_limit_ns();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int box = std::min(page_size, 128);
-  return d == 128 ? launch_attend<128>(ap, pl.tiles, box, st) : launch_attend<64>(ap, pl.tiles, box, st);
+  return d == 128 ? launch_attend<128>(ap, pl.tiles, pl.rows, box, st)
+                  : launch_attend<64>(ap, pl.tiles, pl.rows, box, st);
 }
 
 int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
@@ -268,33 +325,23 @@ int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* 
   if (d != 64 && d != 128) return fail(PIVOT_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
   if (B < 1 || g < 1 || H < 1 || top_k < 1) return fail(PIVOT_ERR_INVALID_ARG, "need B, g, H, top_k >= 1");
   if (static_cast<double>(B) * g * H >= 2147483648.0) return fail(PIVOT_ERR_INVALID_ARG, "B * g * H too large");
-  AttendParams ap{};
+  AttendPagedParams ap{};
   if (int rc = paged_rows(block_table, seqlens, nullptr, B * g, B, g, num_pages, page_size, max_pages, 0x7FFFFFFF, &ap.rows))
     return rc;
   DeviceInfo* dev = nullptr;
   if (int rc = device_info(&dev)) return rc;
   ap.q = static_cast<const uint16_t*>(q);
-  ap.k = static_cast<const uint16_t*>(kpages);
-  ap.v = static_cast<const uint16_t*>(vpages);
+  ap.kpages = static_cast<const uint16_t*>(kpages);
+  ap.vpages = static_cast<const uint16_t*>(vpages);
   ap.idx = idx;
   ap.out = out;
-  ap.R = B * g;
   ap.H = H;
   ap.g = g;
   ap.top_k = top_k;
-  ap.scale = 1.0f / sqrtf(static_cast<float>(d));
+  ap.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(d)));
   ap.status = dev->status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  {
-    TraceScope tr("sparse_attention", st);
-    const unsigned grid = static_cast<unsigned>(static_cast<long long>(ap.R) * H);
-    if (d == 128)
-      sparse_attention_kernel<128, true><<<grid, kAttNT, 0, st>>>(ap);
-    else
-      sparse_attention_kernel<64, true><<<grid, kAttNT, 0, st>>>(ap);
-  }
-  CUDA_TRY(cudaGetLastError());
-  return PIVOT_OK;
+  return d == 128 ? launch_sparse_paged<128>(ap, B, dev->sms, st) : launch_sparse_paged<64>(ap, B, dev->sms, st);
 }
 
 }  // extern "C"

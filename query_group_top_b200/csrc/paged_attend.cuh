@@ -14,11 +14,15 @@
 // axis is split: each CTA takes chunk_of(len) keys, and attend_join_kernel adds up
 // the parts, o = sum_c w_c o_c, w_c = exp(lse_c - lse).
 //
-// attend_rows_kernel is the form for few rows per key head (decode): 16 rows
-// (one m16n8k16 tile), bound by the bytes of the keys and values.  Each of its
-// four warps walks its own 16-key tiles of the chunk with a ring of its own
-// (cp.async, no barrier between warps) and its own (m, l, o), which are merged
-// at the end: nothing waits for anything but memory.
+// attend_rows_kernel is the form for few rows per key head (decode), bound by
+// the bytes of the keys and values.  Each of a CTA's four warps walks its own
+// 16-key steps of the chunk with a ring and an (m, l, o) of its own, merged at
+// the end, so nothing waits for anything but memory.  The products take the
+// keys as the 16 rows of the tile and the queries as its 8 columns:
+//     S^T = K q^T (16 keys x 8 queries), o^T += V^T P^T (16 channels x 8),
+// half the instructions and accumulators of queries in rows; the weights turn
+// from the first product's layout to the second's operand by a transposing
+// register move.
 #pragma once
 
 #include "paged_rows.cuh"
@@ -155,42 +159,121 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], const uint32_t (&a)[
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// An 8 x 8 tile of 16-bit values, two of a row a lane, turned about its diagonal.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 
+// A warp's ring of 16-key steps: 16 key rows and 16 value rows each, 16 bytes
+// apart beyond their length so that the eight rows of a matrix load lie in
+// different banks.  Filled by cp.async, 16 bytes a lane: bulk copies of a row
+// each need one instruction for 32 rows, but took 19 cycles a copy, twice what
+// the memory's rate leaves for 256 bytes.
 template <int D>
-struct RowsCfg {
-  static constexpr int NW = 4;                          // warps, each with keys of its own
-  static constexpr int KT = 16;                         // keys a warp's step
-  static constexpr int ST = D == 128 ? 3 : 6;           // steps in flight per warp
-  static constexpr int TILE = KT * D * 2;               // bytes of a step's keys (its values as many)
-  static constexpr int RING = NW * ST * 2 * TILE;
-  static constexpr int MERGE = NW * 16 * (D + 4) * 4;   // the warps' (o, m, l) at the end, in the ring's place
-  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+struct KvRing {
+  static constexpr int NW = 4;                          // warps a CTA
+  static constexpr int KT = 16;                         // keys a step
+  static constexpr int ROW = 2 * D + 16;
+  static constexpr int HALF = KT * ROW;                 // the keys; the values as many bytes behind them
+  // Steps in flight.  Three CTAs of two steps an SM beat two of three (a decode
+  // step of 64 sequences of 8192, 8 key heads: 378 us for 396) and one of five
+  // (439): a warp's own chain of loads and products wants company.  At 64
+  // channels, four of three beat three of four and five of two (index rows of 32
+  // sequences, 16 heads, 512 indices: 39 us for 47 and 41).
+  static constexpr int ST = D == 128 ? 2 : 3;
+  static constexpr int BYTES = ST * 2 * HALF;           // a warp's ring
+  static constexpr int SMEM = NW * BYTES;
+  static constexpr int PER_SM = D == 128 ? 3 : 4;       // CTAs that an SM holds
+  static_assert(PER_SM * (SMEM + 2048) <= 232448, "shared memory of an SM");
+
+  uint32_t ring;
+  const uint8_t* kbase;                                 // the head's first key row, at the lane's 16 bytes
+  long long to_v;                                       // bytes from a key row to its value row
+  long long stride;                                     // bytes from a cache row to the next
+
+  __device__ __forceinline__ void init(uint8_t* smem, const uint16_t* kpages, const uint16_t* vpages, int heads, int head,
+                                       int warp, int lane) {
+    ring = smem_u32(smem) + warp * BYTES + (lane / (D / 8)) * ROW + (lane % (D / 8)) * 16;
+    kbase = reinterpret_cast<const uint8_t*>(kpages + static_cast<long long>(head) * D + (lane % (D / 8)) * 8);
+    to_v = reinterpret_cast<const uint8_t*>(vpages) - reinterpret_cast<const uint8_t*>(kpages);
+    stride = static_cast<long long>(heads) * D * 2;
+  }
+  // Brings in step `it`: lane l and l + 16 have the cache row of key l, -1
+  // where there is none (zeros then: 0 * what the ring held may be NaN).
+  __device__ __forceinline__ void issue(int it, int row) {
+    const uint32_t dst = ring + (it % ST) * (2 * HALF);
+    constexpr int RP = 256 / D;                         // rows that a warp's 32 pieces make
+#pragma unroll
+    for (int x = 0; x < KT / RP; ++x) {
+      const int kr = __shfl_sync(0xffffffffu, row, x * RP + (threadIdx.x & 31) / (D / 8));
+      const uint8_t* src = kbase + max(kr, 0) * stride;
+      const uint32_t bytes = kr < 0 ? 0u : 16u;
+      cp_async_16(dst + x * RP * ROW, src, bytes);
+      cp_async_16(dst + x * RP * ROW + HALF, src + to_v, bytes);
+    }
+  }
+  __device__ __forceinline__ uint32_t keys(int it, uint8_t* smem, int warp) const {
+    return smem_u32(smem) + warp * BYTES + (it % ST) * (2 * HALF);
+  }
 };
 
+// S^T of a step: s[0], s[1]: key lane / 4 with queries 2 (lane % 4) and the
+// next; s[2], s[3]: key lane / 4 + 8.  Two chains of products, added.
 template <int D>
+__device__ __forceinline__ void step_scores(uint32_t kt, const uint32_t (&qb)[D / 16][2], int lane, float (&s)[4]) {
+  const uint32_t at = kt + ((lane >> 3 & 1) * 8 + (lane & 7)) * KvRing<D>::ROW + (lane >> 4) * 16;
+  float t[2][4] = {};
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    uint32_t a[4];
+    ldmatrix_x4(at + 32 * k, a);
+    mma_m16n8k16(t[k & 1], a, qb[k][0], qb[k][1]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s[e] = t[0][e] + t[1][e];
+}
+// o^T += V^T P^T: o[n]: channel 16 n + lane / 4 (and + 8), queries as above;
+// b0, b1: the weights of keys 0-7 and 8-15, transposed.
+template <int D>
+__device__ __forceinline__ void step_values(uint32_t vt, uint32_t b0, uint32_t b1, int lane, float (&o)[D / 16][4]) {
+  const uint32_t at = vt + ((lane >> 4) * 8 + (lane & 7)) * KvRing<D>::ROW + (lane >> 3 & 1) * 16;
+#pragma unroll
+  for (int n = 0; n < D / 16; ++n) {
+    uint32_t a[4];
+    ldmatrix_x4_trans(at + 32 * n, a);
+    mma_m16n8k16(o[n], a, b0, b1);
+  }
+}
+
+// NT tiles of 8 packed rows a CTA.
+template <int D, int NT>
 __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant__ PagedAttendParams p) {
-  using C = RowsCfg<D>;
-  constexpr int KS = D / 16;       // k-steps of q . k
-  constexpr int CH = D / 8;        // 16-byte pieces of a row
+  using R = KvRing<D>;
+  constexpr int KS = D / 16;       // k-steps of q . k, and 16-channel tiles of o
+  constexpr int ROWS = 8 * NT;
+  constexpr int OS = D + 4;        // floats a row of the merge
+  static_assert(R::NW * ROWS * (OS + 2) * 4 <= R::NW * R::BYTES, "the merge takes the rings' place");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int seq_s[2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   // key heads in the innermost place: neighbouring CTAs read neighbouring heads of the same rows
-  const long long bid = blockIdx.x;
+  const unsigned bid = blockIdx.x;
   const int hk = static_cast<int>(bid % p.Hk);
   const int split = static_cast<int>(bid / p.Hk % p.nsplit);
   const int flat = static_cast<int>(bid / p.Hk / p.nsplit);
   if (warp == 0) {
     int tile = 0;
-    const int b = locate_tile(p.rows, p.grp, 16, flat, lane, &tile, p.status);
+    const int b = locate_tile(p.rows, p.grp, ROWS, flat, lane, &tile, p.status);
     if (lane == 0) seq_s[0] = b, seq_s[1] = tile;
   }
   __syncthreads();
-  const int b = seq_s[0], r0 = seq_s[1] * 16;
+  const int b = seq_s[0], r0 = seq_s[1] * ROWS;
   if (b < 0) return;
   const NewSpan sp = p.rows.span(b);
-  const int nrows = min(16, sp.n * p.grp - r0);
+  const int nrows = min(ROWS, sp.n * p.grp - r0);
   if (nrows <= 0) return;
   const int pos0 = sp.len - sp.n + p.self_key;             // lim of the sequence's first new token
   auto lim_of = [&](int r) { return sp.ok ? pos0 + (r0 + r) / p.grp : 0; };
@@ -203,160 +286,136 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
   const int kend = min(lim_of(nrows - 1), kbeg + chunk);
   if (kbeg >= kend && split > 0) return;                   // the join reads no part a row has no keys in
 
-  const int gr = lane >> 2, gc = lane & 3;                 // row and column group of the mma fragments
-  uint32_t qa[KS][4];
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    const int r = gr + 8 * hf;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + row_of(r < nrows ? r : 0) * D) + gc;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      qa[k][hf] = r < nrows ? src[8 * k] : 0u;
-      qa[k][2 + hf] = r < nrows ? src[8 * k + 4] : 0u;
-    }
-  }
-  const int lim0 = lim_of(gr), lim1 = lim_of(gr + 8);
-
-  const uint32_t ring = smem_u32(smem) + warp * (C::ST * 2 * C::TILE);
-  const int ntiles = (kend - kbeg + C::KT - 1) / C::KT;    // of the CTA; the warp takes every NW-th
-  const int mine = ntiles > warp ? (ntiles - warp + C::NW - 1) / C::NW : 0;
-  // cache row of the key that lanes l and l + 16 address in tile `it`
-  auto key_row = [&](int it) -> long long {
-    const int j = kbeg + (warp + it * C::NW) * C::KT + (lane & 15);
+  const int ntiles = max(0, (kend - kbeg + R::KT - 1) / R::KT);   // of the CTA; the warp takes every NW-th
+  const int mine = ntiles > warp ? (ntiles - warp + R::NW - 1) / R::NW : 0;
+  R kv;
+  kv.init(smem, p.kpages, p.vpages, p.Hk, hk, warp, lane);
+  // cache row of the key that lanes l and l + 16 address in step `it`
+  auto place = [&](int it) -> int {
+    const int j = kbeg + (warp + it * R::NW) * R::KT + (lane & 15);
     if (it >= mine || j >= kend) return -1;
     const long long row = p.rows.row(b, j);
     if (row < 0) atomicOr(p.status, kStBadPage);
-    return row;
+    return static_cast<int>(row);
   };
-  long long next_row = key_row(0);
+  int next = place(0);
   auto issue = [&](int it) {
-    const long long row = next_row;
-    next_row = key_row(it + 1);
-    if (it < mine) {
-      const uint32_t dst = ring + (it % C::ST) * (2 * C::TILE);
-#pragma unroll
-      for (int x = 0; x < C::KT * CH / 32; ++x) {
-        const int key = (x * 32 + lane) / CH, ch = lane % CH;
-        const long long kr = __shfl_sync(0xffffffffu, row, key);
-        const long long off = kr < 0 ? 0 : (kr * p.Hk + hk) * D + ch * 8;
-        const uint32_t to = dst + key * (D * 2) + ((ch ^ (key & 7)) << 4);
-        cp_async_16(to, p.kpages + off, kr < 0 ? 0u : 16u);
-        cp_async_16(to + C::TILE, p.vpages + off, kr < 0 ? 0u : 16u);
-      }
-    }
+    const int row = next;
+    next = place(it + 1);
+    if (it < mine) kv.issue(it, row);
     cp_async_commit();
   };
+#pragma unroll
+  for (int s = 0; s < R::ST - 1; ++s) issue(s);
 
-  float o[CH][4], m0 = neg_inf(), m1 = neg_inf(), l0 = 0.f, l1 = 0.f;
+  const int gr = lane >> 2, gc = lane & 3;
+  uint32_t qb[NT][KS][2];
+  int lim[NT][2];
 #pragma unroll
-  for (int n = 0; n < CH; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  for (int t = 0; t < NT; ++t) {
+    const int r = 8 * t + gr;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + row_of(r < nrows ? r : 0) * D) + gc;
 #pragma unroll
-  for (int s = 0; s < C::ST - 1; ++s) issue(s);
-  const int lrow = lane & 7, lmat = lane >> 3;
+    for (int k = 0; k < KS; ++k) {
+      qb[t][k][0] = r < nrows ? src[8 * k] : 0u;
+      qb[t][k][1] = r < nrows ? src[8 * k + 4] : 0u;
+    }
+    lim[t][0] = min(kend, lim_of(8 * t + 2 * gc));
+    lim[t][1] = min(kend, lim_of(8 * t + 2 * gc + 1));
+  }
+  float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t][0] = m[t][1] = neg_inf();
+    l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < KS; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+  }
   for (int it = 0; it < mine; ++it) {
-    issue(it + C::ST - 1);
-    cp_async_wait<C::ST - 1>();
+    issue(it + R::ST - 1);
+    cp_async_wait<R::ST - 1>();
     __syncwarp();
-    const uint32_t kt = ring + (it % C::ST) * (2 * C::TILE), vt = kt + C::TILE;
-    float s[2][4] = {};
-    {
-      const int key = (lmat >> 1) * 8 + lrow;
+    const uint32_t kt = kv.keys(it, smem, warp);
+    const int j = kbeg + (warp + it * R::NW) * R::KT + gr;
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t kb[4];
-        ldmatrix_x4(kt + key * (D * 2) + (((2 * k + (lmat & 1)) ^ (key & 7)) << 4), kb);
-        mma_m16n8k16(s[0], qa[k], kb[0], kb[1]);
-        mma_m16n8k16(s[1], qa[k], kb[2], kb[3]);
-      }
-    }
-    const int j0 = kbeg + (warp + it * C::NW) * C::KT + 2 * gc;
-    float x0 = neg_inf(), x1 = neg_inf();
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int t = 0; t < NT; ++t) {
+      float s[4];
+      step_scores<D>(kt, qb[t], lane, s);
+      float x[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = j0 + 8 * n + e;
-        s[n][e] = j < lim0 && j < kend ? s[n][e] * p.scale_log2 : neg_inf();
-        s[n][2 + e] = j < lim1 && j < kend ? s[n][2 + e] * p.scale_log2 : neg_inf();
-        x0 = fmaxf(x0, s[n][e]);
-        x1 = fmaxf(x1, s[n][2 + e]);
+        s[e] = j < lim[t][e] ? s[e] * p.scale_log2 : neg_inf();
+        s[2 + e] = j + 8 < lim[t][e] ? s[2 + e] * p.scale_log2 : neg_inf();
+        x[e] = fmaxf(s[e], s[2 + e]);
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], y));
       }
-    }
+      if (__any_sync(0xffffffffu, x[0] > m[t][0] || x[1] > m[t][1])) {
+        float f[2];
 #pragma unroll
-    for (int x = 1; x <= 2; x <<= 1) {
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, x));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, x));
-    }
-    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-      const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      const float f0 = m0 == n0 ? 1.f : fast_exp2(m0 - n0), f1 = m1 == n1 ? 1.f : fast_exp2(m1 - n1);
-      m0 = n0, m1 = n1;
-      l0 *= f0, l1 *= f1;
+        for (int e = 0; e < 2; ++e) {
+          const float n = fmaxf(m[t][e], x[e]);
+          f[e] = m[t][e] == n ? 1.f : fast_exp2(m[t][e] - n);
+          m[t][e] = n;
+          l[t][e] *= f[e];
+        }
 #pragma unroll
-      for (int n = 0; n < CH; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
-    }
-    const float z0 = m0 == neg_inf() ? 0.f : m0, z1 = m1 == neg_inf() ? 0.f : m1;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < KS; ++n)
+          o[t][n][0] *= f[0], o[t][n][1] *= f[1], o[t][n][2] *= f[0], o[t][n][3] *= f[1];
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        s[n][e] = fast_exp2(s[n][e] - z0);
-        s[n][2 + e] = fast_exp2(s[n][2 + e] - z1);
-        l0 += s[n][e];
-        l1 += s[n][2 + e];
+        const float z = m[t][e] == neg_inf() ? 0.f : m[t][e];
+        s[e] = fast_exp2(s[e] - z);
+        s[2 + e] = fast_exp2(s[2 + e] - z);
+        l[t][e] += s[e] + s[2 + e];
       }
-    }
-    // the weights go to bf16 for the second product, as its operand type asks; their sum l stays fp32
-    const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                            pack_bf16(s[1][2], s[1][3])};
-    {
-      const int key = (lmat & 1) * 8 + lrow;
-#pragma unroll
-      for (int n = 0; n < CH; n += 2) {
-        uint32_t vb[4];
-        ldmatrix_x4_trans(vt + key * (D * 2) + (((n + (lmat >> 1)) ^ (key & 7)) << 4), vb);
-        mma_m16n8k16(o[n], pa, vb[0], vb[1]);
-        mma_m16n8k16(o[n + 1], pa, vb[2], vb[3]);
-      }
+      // the weights go to bf16 for the second product, as its operand type asks; their sum l stays fp32
+      step_values<D>(kt + R::HALF, transpose_8x8(pack_bf16(s[0], s[1])), transpose_8x8(pack_bf16(s[2], s[3])), lane, o[t]);
     }
     __syncwarp();   // every lane has read the slot that the next step's copies fill
   }
   cp_async_wait<0>();
 #pragma unroll
-  for (int x = 1; x <= 2; x <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-  }
-  __syncthreads();
-  // merge the warps' parts: [warp][row][D] and the rows' (m, l) behind them
-  float* mo = reinterpret_cast<float*>(smem);
-  float* ml = mo + C::NW * 16 * D;
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-  for (int n = 0; n < CH; ++n) {
-    float* at = mo + (warp * 16 + gr) * D + 8 * n + 2 * gc;
-    *reinterpret_cast<float2*>(at) = make_float2(o[n][0], o[n][1]);
-    *reinterpret_cast<float2*>(at + 8 * D) = make_float2(o[n][2], o[n][3]);
-  }
-  if (gc == 0) {
-    *reinterpret_cast<float2*>(ml + (warp * 16 + gr) * 2) = make_float2(m0, l0);
-    *reinterpret_cast<float2*>(ml + (warp * 16 + gr + 8) * 2) = make_float2(m1, l1);
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int y = 4; y < 32; y <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], y);
+  __syncthreads();
+  // merge the warps' parts: [warp][row][OS] and the rows' (m, l) behind them
+  float* mo = reinterpret_cast<float*>(smem);
+  float* ml = mo + R::NW * ROWS * OS;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float* at = mo + (warp * ROWS + 8 * t + 2 * gc + (e & 1)) * OS + gr + 8 * (e >> 1);
+#pragma unroll
+      for (int n = 0; n < KS; ++n) at[16 * n] = o[t][n][e];
+    }
+    if (gr == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float2*>(ml + (warp * ROWS + 8 * t + 2 * gc + e) * 2) = make_float2(m[t][e], l[t][e]);
+    }
   }
   __syncthreads();
   constexpr int CL = D / 32;
-  for (int r = warp; r < nrows; r += C::NW) {
-    float m = neg_inf(), l = 0.f, acc[CL] = {};
+  for (int r = warp; r < nrows; r += R::NW) {
+    float rm = neg_inf(), rl = 0.f, acc[CL] = {};
 #pragma unroll
-    for (int w = 0; w < C::NW; ++w) m = fmaxf(m, ml[(w * 16 + r) * 2]);
-    const float z = m == neg_inf() ? 0.f : m;
+    for (int w = 0; w < R::NW; ++w) rm = fmaxf(rm, ml[(w * ROWS + r) * 2]);
+    const float z = rm == neg_inf() ? 0.f : rm;
 #pragma unroll
-    for (int w = 0; w < C::NW; ++w) {
-      const float f = fast_exp2(ml[(w * 16 + r) * 2] - z);
-      l = fmaf(f, ml[(w * 16 + r) * 2 + 1], l);
+    for (int w = 0; w < R::NW; ++w) {
+      const float f = fast_exp2(ml[(w * ROWS + r) * 2] - z);
+      rl = fmaf(f, ml[(w * ROWS + r) * 2 + 1], rl);
 #pragma unroll
-      for (int c = 0; c < CL; ++c) acc[c] = fmaf(f, mo[(w * 16 + r) * D + lane * CL + c], acc[c]);
+      for (int c = 0; c < CL; ++c) acc[c] = fmaf(f, mo[(w * ROWS + r) * OS + lane * CL + c], acc[c]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    float lse2 = l == 0.f ? neg_inf() : m + log2f(l);
+    const float inv = rl == 0.f ? 0.f : 1.f / rl;
+    float lse2 = rl == 0.f ? neg_inf() : rm + log2f(rl);
     bool fine = true;
 #pragma unroll
     for (int c = 0; c < CL; ++c) {

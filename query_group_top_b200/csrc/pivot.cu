@@ -26,6 +26,7 @@
 
 #include "../../include/pivot.h"
 #include "attend.cuh"
+#include "attend_paged.cuh"
 #include "finalize.cuh"
 #include "paged_attend_tc.cuh"
 #include "proxy_decode.cuh"
@@ -802,9 +803,9 @@ int pivot_sparse_attention(const void* q, const void* k, const void* v, const in
     TraceScope tr("sparse_attention", st);
     const unsigned grid = static_cast<unsigned>(static_cast<long long>(R) * H);
     if (d == 128)
-      sparse_attention_kernel<128, false><<<grid, kAttNT, 0, st>>>(ap);
+      sparse_attention_kernel<128><<<grid, kAttNT, 0, st>>>(ap);
     else
-      sparse_attention_kernel<64, false><<<grid, kAttNT, 0, st>>>(ap);
+      sparse_attention_kernel<64><<<grid, kAttNT, 0, st>>>(ap);
   }
   CUDA_TRY(cudaGetLastError());
   return PIVOT_OK;
