@@ -205,8 +205,9 @@ int pivot_decode_index_paged(const void* q, const void* kpages, const int32_t* b
  *    two, fewer than 2^31 rows; block_table: int32 [B][max_pages] (device).
  *  - The device arrays are checked where they are used: a sequence whose lengths
  *    contradict each other or exceed max_pages * page_size (or max_seqlen, where
- *    given) is skipped, and so is a row whose page is not in [0, num_pages); both
- *    are reported by pivot_sync_status() as PIVOT_ERR_INVALID_ARG.
+ *    given) is skipped; a row whose page is not in [0, num_pages) is not written,
+ *    and read as zeros; both are reported by pivot_sync_status() as
+ *    PIVOT_ERR_INVALID_ARG.
  *  - d is 64 or 128.  fp32 arithmetic; each result is rounded once.
  */
 
@@ -283,7 +284,7 @@ typedef struct {
  * longer sequence is skipped.  Keys and values that a query does not see may
  * hold anything.  workspace as in the _ws variants; the size may be 0.
  */
-size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int page_size, int max_seqlen);
+size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int max_seqlen);
 int pivot_paged_attention(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
                           const int32_t* seqlens, const int32_t* cu_q, const pivot_attend_t* options, int T, int B,
                           int Hq, int Hk, int d, int g, int num_pages, int page_size, int max_pages, int max_seqlen,

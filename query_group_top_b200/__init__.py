@@ -102,7 +102,7 @@ def load_library():
         "pivot_set_wait_limit": ([ctypes.c_ulonglong], I),
         "pivot_qk_rope": ([P, P, I, P, P, I, I, P, P, P], I),
         "pivot_paged_append": ([P, P, P, I, P, P, P, P, I, I, I, I, I, I, I, P, P, P, P], I),
-        "pivot_paged_attention_workspace_size": ([I, I, I, I, I, I, I], Z),
+        "pivot_paged_attention_workspace_size": ([I, I, I, I, I, I], Z),
         "pivot_paged_attention": ([P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P, P, Z, P], I),
         "pivot_sparse_attention_paged": ([P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P], I),
     }
@@ -638,7 +638,7 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
         if out_lse is not None:
             plse = _out(out_lse, q.shape[:-1], torch.float32, device, "out_lse").data_ptr()
         if T and B:
-            nbytes = lib.pivot_paged_attention_workspace_size(T, B, Hq, Hk, d, page, max_seqlen)
+            nbytes = lib.pivot_paged_attention_workspace_size(T, B, Hq, Hk, d, max_seqlen)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
             rc = lib.pivot_paged_attention(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pcu, opt, T, B,
                                            Hq, Hk, d, g, n, page, max_pages, max_seqlen, out.data_ptr(), plse,

@@ -55,10 +55,23 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
   const int b = static_cast<int>(rh / p.H / p.g);
   const int len = min(p.rows.seqlens[b], p.rows.max_len);
   const int chunk = ((p.top_k + p.parts - 1) / p.parts + 15) & ~15;
-  const int tbeg = rank * chunk, tend = min(p.top_k, tbeg + chunk);
+  const int tbeg = rank * chunk;
+  int tend = min(p.top_k, tbeg + chunk);
   const int32_t* row = p.idx + static_cast<long long>(rh) * p.top_k;
   R kv;
   kv.init(smem, p.kpages, p.vpages, p.H, h, warp, lane);
+  {
+    // the part ends behind its last index: rows are often padded far beyond their sequence
+    __shared__ int last_s[R::NW];
+    int last = tbeg;
+#pragma unroll 4
+    for (int t = tbeg + threadIdx.x; t < tend; t += 128)
+      if (__ldg(row + t) >= 0) last = t + 1;
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0) last_s[warp] = last;
+    __syncthreads();
+    tend = max(max(last_s[0], last_s[1]), max(last_s[2], last_s[3]));
+  }
 
   const int ntiles = tend > tbeg ? (tend - tbeg + R::KT - 1) / R::KT : 0;
   const int mine = ntiles > warp ? (ntiles - warp + R::NW - 1) / R::NW : 0;

@@ -131,11 +131,10 @@ struct AttendPlan {
   size_t part_lse, total;   // workspace: the parts' rows at 0, their lse at part_lse
 };
 
-AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int page_size, int max_seqlen, int sms) {
+AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int sms) {
   AttendPlan a{};
   const long long rows = static_cast<long long>(T) * (Hq / Hk);
-  // TMA lays boxes of 8 rows or more into the swizzled tiles, so smaller pages go to the rows kernel
-  a.tiles = rows >= 32ll * B && page_size >= 8;
+  a.tiles = rows >= 32ll * B;
   a.rows = a.tiles ? 256 : rows <= 8ll * B ? 8 : 16;
   a.min_chunk = a.tiles ? 512 : 256;
   const long long ctas = std::max<long long>(B, (rows + a.rows - 1) / a.rows) * Hk;
@@ -156,16 +155,21 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int page_size, int m
 }
 
 template <int D>
-int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, int box_rows, cudaStream_t st) {
+int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(static_cast<long long>(ap.tiles) * ap.Hk * ap.nsplit);
   if (tiles) {
-    CUtensorMap mk, mv;
-    const int rows = ap.rows.num_pages << ap.rows.log2_page;
-    if (int rc = make_rows_map(&mk, ap.kpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
-    if (int rc = make_rows_map(&mv, ap.vpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
-    if (int rc = allow_smem<attend_tiles_kernel<D>>(TcCfg<D>::SMEM)) return rc;
+    CUtensorMap mk{}, mv{};
     TraceScope tr("attend_tiles", st);
-    attend_tiles_kernel<D><<<grid, TcCfg<D>::THREADS, TcCfg<D>::SMEM, st>>>(mk, mv, ap);
+    if (ap.rows.log2_page < 3) {
+      if (int rc = allow_smem<attend_tiles_kernel<D, true>>(TcCfg<D>::SMEM)) return rc;
+      attend_tiles_kernel<D, true><<<grid, TcCfg<D>::THREADS, TcCfg<D>::SMEM, st>>>(mk, mv, ap);
+    } else {
+      const int rows = ap.rows.num_pages << ap.rows.log2_page, box_rows = std::min(1 << ap.rows.log2_page, 128);
+      if (int rc = make_rows_map(&mk, ap.kpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
+      if (int rc = make_rows_map(&mv, ap.vpages, rows, ap.Hk, ap.Hk, D, box_rows)) return rc;
+      if (int rc = allow_smem<attend_tiles_kernel<D, false>>(TcCfg<D>::SMEM)) return rc;
+      attend_tiles_kernel<D, false><<<grid, TcCfg<D>::THREADS, TcCfg<D>::SMEM, st>>>(mk, mv, ap);
+    }
   } else {
     TraceScope tr("attend_rows", st);
     if (rows_per_cta == 8) {
@@ -179,8 +183,16 @@ int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, int
   CUDA_TRY(cudaGetLastError());
   if (ap.nsplit > 1) {
     TraceScope tr("attend_join", st);
-    const long long rows = static_cast<long long>(ap.rows.T) * ap.Hq;
-    attend_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(ap);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(ap.rows.T) * ap.Hq + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    CUDA_TRY(cudaLaunchKernelEx(&cfg, attend_join_kernel<D>, ap));
   }
   CUDA_TRY(cudaGetLastError());
   return PIVOT_OK;
@@ -261,9 +273,9 @@ int pivot_paged_append(const pivot_heads_t* k, const pivot_heads_t* v, const piv
   return run_rope(rp, dtype, rope, d, static_cast<cudaStream_t>(stream));
 }
 
-size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int page_size, int max_seqlen) {
-  if (T < 1 || B < 1 || Hk < 1 || Hq < Hk || d < 1 || page_size < 1 || max_seqlen < 1) return 0;
-  return plan_attend(T, B, Hq, Hk, d, page_size, max_seqlen, device_sms()).total;
+size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int max_seqlen) {
+  if (T < 1 || B < 1 || Hk < 1 || Hq < Hk || d < 1 || max_seqlen < 1) return 0;
+  return plan_attend(T, B, Hq, Hk, d, max_seqlen, device_sms()).total;
 }
 
 int pivot_paged_attention(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
@@ -285,7 +297,7 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   if (static_cast<long long>(T) * (Hq / Hk) >= (1ll << 31) - 32) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
   DeviceInfo* dev = nullptr;
   if (int rc = device_info(&dev)) return rc;
-  const AttendPlan pl = plan_attend(T, B, Hq, Hk, d, page_size, max_seqlen, dev->sms);
+  const AttendPlan pl = plan_attend(T, B, Hq, Hk, d, max_seqlen, dev->sms);
   if (pl.total > workspace_bytes || (pl.total && !workspace))
     return fail(PIVOT_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", pl.total, workspace_bytes);
   if (pl.total && (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
@@ -311,9 +323,7 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   ap.status = dev->status;
   ap.wait_ns = wait_limit_ns();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int box = std::min(page_size, 128);
-  return d == 128 ? launch_attend<128>(ap, pl.tiles, pl.rows, box, st)
-                  : launch_attend<64>(ap, pl.tiles, pl.rows, box, st);
+  return d == 128 ? launch_attend<128>(ap, pl.tiles, pl.rows, st) : launch_attend<64>(ap, pl.tiles, pl.rows, st);
 }
 
 int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,

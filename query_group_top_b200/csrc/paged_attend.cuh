@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
   __shared__ int seq_s[2];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  grid_launch_dependents();
   // key heads in the innermost place: neighbouring CTAs read neighbouring heads of the same rows
   const unsigned bid = blockIdx.x;
   const int hk = static_cast<int>(bid % p.Hk);
@@ -441,7 +442,8 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------ joining the parts
 // One warp a row: the parts that hold keys of the row are the first
-// ceil(lim / chunk_of(len)) (at least one), whichever kernel wrote them.
+// ceil(lim / chunk_of(len)) (at least one), whichever kernel wrote them.  Launched
+// while that kernel still runs, it looks its row up and then waits for it.
 template <int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ PagedAttendParams p) {
   constexpr int CL = D / 32;
@@ -455,6 +457,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const int lim = sp.ok ? sp.len - sp.n + p.self_key + (tok - sp.tok0) : 0;
   const int chunk = chunk_of(sp.len, p);
   const int parts = max(1, (lim + chunk - 1) / chunk);
+  grid_wait();
   float m = neg_inf();
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_lse[s * rows + row]);
 #pragma unroll

@@ -8,6 +8,9 @@
 //               brings keys and values in by TMA, one box per page and 64
 //               channels (a page of 128 rows or more: per tile), through one
 //               ring of key and value tiles
+//   warps 2, 3  the producer for pages of fewer than 8 rows (GATHER), which TMA
+//               cannot lay into the swizzled tiles: every key row looked up by
+//               itself and copied in 16-byte pieces (cp.async)
 //   warp 1      TMEM allocator and MMA issuer (one elected thread):
 //               S_t = Q_t K^T (128 x 128 x d), O_t += P_t V (128 x d x 128),
 //               P_t read from TMEM, V as it lies (keys in rows: N-major)
@@ -83,7 +86,7 @@ __device__ __forceinline__ void exp2_poly(float xa, float xb, float& a, float& b
   b = __uint_as_float((__float_as_uint(nb) << 23) + __float_as_uint(rb));
 }
 
-template <int D>
+template <int D, bool GATHER>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ PagedAttendParams p) {
@@ -109,6 +112,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   int* seq_s = reinterpret_cast<int*>(smem + C::OFF_BAR + 232);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  grid_launch_dependents();
   // key heads innermost (neighbouring CTAs share pages), the longest row tiles first
   const unsigned bid = blockIdx.x;
   const int hk = static_cast<int>(bid % p.Hk);
@@ -121,7 +125,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       seq_s[0] = b;
       seq_s[1] = tile;
       for (int s = 0; s < C::NST; ++s) {
-        mbar_init(full_bar(s), 1);
+        mbar_init(full_bar(s), GATHER ? 64 : 1);
         mbar_init(empty_bar(s), 1);
       }
       mbar_init(q_bar, 256);
@@ -163,7 +167,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if (warp < 4) {
     regs_dec<C::REGS_FEW>();
   }
-  if (warp == 0) {
+  if (!GATHER && warp == 0) {
     // ------------------------------------------------------------ producer
     const int end = max(kend[0], kend[1]);
     const int page_rows = min(1 << p.rows.log2_page, C::BN);
@@ -244,6 +248,54 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // never leave the CTA with a copy still landing in its shared memory
     if (tail_used) mbar_wait_cleanup(tail_bar, 0);
     for (int u = max(0, use - C::NST); u < use; ++u) mbar_wait_cleanup(full_bar(u % C::NST), (u / C::NST) & 1);
+  } else if (GATHER && (warp == 2 || warp == 3)) {
+    // ------------------------------------------------------------ producers, row by row
+    constexpr int CH = D / 8, RP = 32 / CH;                 // pieces of a row, rows that a warp's 32 pieces make
+    const int end = max(kend[0], kend[1]);
+    const int ch = lane % CH, kw = (warp - 2) * 64;         // the lane's piece; the warp's first key of a tile
+    const uint16_t* kb = p.kpages + static_cast<long long>(hk) * D + ch * 8;
+    const uint16_t* vb = p.vpages + static_cast<long long>(hk) * D + ch * 8;
+    const long long stride = static_cast<long long>(p.Hk) * D;
+    // cache row of key kw + 32 half + lane of tile i, -1: none (its rows become zeros)
+    auto key_row = [&](int i, int half) -> int {
+      const int j = kbeg + i * C::BN + kw + 32 * half + lane;
+      if (i >= n || j >= end) return -1;
+      const long long row = p.rows.row(b, j);
+      if (row < 0) atomicOr(p.status, kStBadPage);
+      return static_cast<int>(row);
+    };
+    int use = 0;
+    bool ok = true;
+    auto fill = [&](const uint16_t* base, int r0_, int r1_) {
+      const int s = use % C::NST, u = use / C::NST;
+      if (u > 0) {
+        ok = mbar_wait(empty_bar(s), (u - 1) & 1, abort_flag, p.status, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+      }
+      const uint32_t dst = ring + s * C::TILE + (ch >> 3) * C::ATOM;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll 8
+        for (int x = 0; x < 32 / RP; ++x) {
+          const int k = x * RP + lane / CH, key = kw + 32 * half + k;
+          const int row = __shfl_sync(0xffffffffu, half ? r1_ : r0_, k);
+          cp_async_16(dst + key * 128 + (((ch & 7) ^ (key & 7)) << 4), base + max(row, 0) * stride, row < 0 ? 0u : 16u);
+        }
+      }
+      cp_async_arrive_noinc(full_bar(s));
+      ++use;
+    };
+    int n0 = key_row(0, 0), n1 = key_row(0, 1);
+    for (int i = 0; i < n && ok; ++i) {
+      const int c0 = n0, c1 = n1;
+      n0 = key_row(i + 1, 0);
+      n1 = key_row(i + 1, 1);
+      fill(kb, c0, c1);
+      if (ok) fill(vb, c0, c1);
+    }
+    // never leave the CTA with a copy still landing in its shared memory
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp walks the loop and one lane issues: a loop of one lane
@@ -289,6 +341,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       };
       bool ok = wait(q_bar, 0) && wait(full_bar(0), 0);
       if (ok) {
+        if (GATHER) fence_proxy_async_smem();               // the rows were written by threads, the products read them
         tc_fence_after();
         if (elect_one()) {
           if (n0 > 0) scores(0, 0);
@@ -312,6 +365,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           ok = wait(full_bar(vs), vph) && (!more || wait(full_bar(ks), kph));
           if (!ok) break;
         }
+        if (GATHER) fence_proxy_async_smem();
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int nt = t == 0 ? n0 : n1;

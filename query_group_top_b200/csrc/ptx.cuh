@@ -288,6 +288,13 @@ __device__ __forceinline__ void tmem_ld_wait() {
 // Pins a register value after tmem_ld_wait so no use is scheduled before the wait.
 __device__ __forceinline__ void reg_fence(uint32_t& v) { asm volatile("" : "+r"(v)); }
 
+// ------------------------------------------------------------------ dependent launches
+// Lets a kernel launched behind this one (programmatic stream serialisation)
+// start once every CTA has come here; what this one writes is there for it
+// only behind grid_wait.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ register shares, paired fp32
 // Moves registers between the warpgroups of a CTA; every warp of the warpgroup
 // calls it.  The shares must add up to no more than the CTA was launched with.

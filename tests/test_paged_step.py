@@ -98,8 +98,8 @@ def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 64, 1, 1, 1, 1, 0, ptr, None) == 1
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 32, 1, 1, 1, 1, 1, ptr, None) == 2
     # the workspace is host arithmetic: parts of a long axis for few rows, none where the rows fill the device
-    assert lib.pivot_paged_attention_workspace_size(2, 1, 16, 16, 128, 16, 131072) >= 2 * 2 * 16 * 129 * 4
-    assert lib.pivot_paged_attention_workspace_size(0, 1, 16, 16, 128, 16, 131072) == 0
+    assert lib.pivot_paged_attention_workspace_size(2, 1, 16, 16, 128, 131072) >= 2 * 2 * 16 * 129 * 4
+    assert lib.pivot_paged_attention_workspace_size(0, 1, 16, 16, 128, 131072) == 0
 
 
 @pytest.fixture(scope="module")
@@ -384,6 +384,8 @@ ATTEND = [  # held, new, Hq, Hk, d, page, itself, ragged
     ([5000, 0], [50, 33], 8, 2, 64, 512, True, True),
     ([127, 128, 129, 255, 256, 257], [1] * 6, 2, 1, 128, 128, True, True),
     ([90], [40], 5, 1, 64, 2, True, True),
+    ([1300, 0], [41, 300], 4, 2, 128, 1, True, True),              # matrix tiles over pages of one row
+    ([600], [77], 3, 3, 64, 4, False, False),
     (list(range(0, 80, 2)), [1 + i % 2 for i in range(40)], 2, 2, 64, 16, True, True),
 ]
 
@@ -428,11 +430,11 @@ def test_paged_attention(case):
 
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("new", [2, 40])
-def test_paged_attention_masked_values_may_be_anything(new, d):
+@pytest.mark.parametrize("page,new", [(16, 2), (16, 40), (2, 40)])
+def test_paged_attention_masked_values_may_be_anything(page, new, d):
     """A key or value that a query does not see leaves it alone, infinity and NaN included, also where both share a
     tile; the queries that see it take it."""
-    H, held, page = 2, 60, 16
+    H, held = 2, 60
     c = ref.Cache([held], [new], H, d, page, seed=5)
     q = normal((new, H, d), 41)
     clean, _ = attend(c, q, True, True)
