@@ -109,15 +109,22 @@ int check_dtype(int dtype) {
 }
 
 // How many parts to cut `units` equal pieces of work of `len` keys into, where
-// the device takes `slots` at a time and a part costs as much as `fixed` keys
-// more: the rounds it takes times a part's length.  A cut that leaves a last
-// round nearly empty costs that round (64 sequences, 8 key heads, 8192 keys in
-// 2 parts: 396 us; in 4: 350).
-int best_parts(long long units, long long slots, long long len, long long fixed, long long most) {
+// the device takes `slots` at a time: the rounds it takes times a part's time
+// (its keys and a fixed part), and the join's (its launch, and the parts' rows
+// through memory).  Times in ns.  A cut that leaves a last round nearly empty
+// costs that round (64 sequences, 8 key heads, 8192 keys in 2 parts: 396 us; in
+// 4: 350); a cut of many rows costs their parts' bytes.
+struct PartCost {
+  double per_key, fixed, join, join_per_part;
+};
+int best_parts(long long units, long long slots, long long len, const PartCost& c, long long most) {
   most = std::min(most, std::max(1ll, 8 * slots / units));
-  long long best = 1, least = -1;
+  long long best = 1;
+  double least = -1;
   for (long long n = 1; n <= most; ++n) {
-    const long long cost = (units * n + slots - 1) / slots * ((len + n - 1) / n + fixed);
+    const double cost = static_cast<double>((units * n + slots - 1) / slots) *
+                            (static_cast<double>((len + n - 1) / n) * c.per_key + c.fixed) +
+                        (n > 1 ? c.join + static_cast<double>(n) * c.join_per_part : 0.0);
     if (least < 0 || cost < least) least = cost, best = n;
   }
   return static_cast<int>(best);
@@ -136,15 +143,18 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int 
   const long long rows = static_cast<long long>(T) * (Hq / Hk);
   a.tiles = rows >= 32ll * B;
   a.rows = a.tiles ? 256 : rows <= 8ll * B ? 8 : 16;
-  a.min_chunk = a.tiles ? 512 : 256;
-  const long long ctas = std::max<long long>(B, (rows + a.rows - 1) / a.rows) * Hk;
+  a.min_chunk = 256;
+  const long long ctas = B * ((rows + static_cast<long long>(B) * a.rows - 1) / (static_cast<long long>(B) * a.rows)) * Hk;
+  const long long most = (max_seqlen + a.min_chunk - 1) / a.min_chunk;
+  const double part_bytes = static_cast<double>(T) * Hq * d * 8;   // a part of every row written and read
   if (a.tiles) {
-    a.nsplit = static_cast<int>(std::min<long long>(std::max<long long>(1, 2ll * sms / ctas),
-                                                    (max_seqlen + a.min_chunk - 1) / a.min_chunk));
+    // a key tile of both row tiles takes 1.4 us (1.1 at 64 channels), what comes before and after some 6 us
+    a.nsplit = best_parts(ctas, sms, max_seqlen, PartCost{(d == 128 ? 1400. : 1100.) / 128, 6000, 6000, part_bytes / 5000}, most);
   } else {
+    // an SM's share of the memory's rate, among its CTAs; some 3 us before and after
     const int per_sm = d == 128 ? KvRing<128>::PER_SM : KvRing<64>::PER_SM;
-    a.nsplit = best_parts(ctas, static_cast<long long>(per_sm) * sms, max_seqlen, 96,
-                          (max_seqlen + a.min_chunk - 1) / a.min_chunk);
+    a.nsplit = best_parts(ctas, static_cast<long long>(per_sm) * sms, max_seqlen,
+                          PartCost{4. * d / 41. * per_sm, 3300, 4500, part_bytes / 5000}, most);
   }
   if (a.nsplit > 1) {
     const size_t parts = static_cast<size_t>(a.nsplit) * T * Hq;
@@ -184,7 +194,9 @@ int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, cud
   if (ap.nsplit > 1) {
     TraceScope tr("attend_join", st);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(ap.rows.T) * ap.Hq + 3) / 4));
+    const long long rows = static_cast<long long>(ap.rows.T) * ap.Hq;
+    const bool wide = ap.nsplit > 4;
+    cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -192,7 +204,8 @@ int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, cud
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    CUDA_TRY(cudaLaunchKernelEx(&cfg, attend_join_kernel<D>, ap));
+    CUDA_TRY(wide ? cudaLaunchKernelEx(&cfg, attend_join_kernel<D, true>, ap)
+                  : cudaLaunchKernelEx(&cfg, attend_join_kernel<D, false>, ap));
   }
   CUDA_TRY(cudaGetLastError());
   return PIVOT_OK;

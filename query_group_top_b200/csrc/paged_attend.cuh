@@ -441,14 +441,18 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ joining the parts
-// One warp a row: the parts that hold keys of the row are the first
+// The parts that hold keys of the row are the first
 // ceil(lim / chunk_of(len)) (at least one), whichever kernel wrote them.  Launched
 // while that kernel still runs, it looks its row up and then waits for it.
-template <int D>
+// WIDE: a CTA's four warps share a row's parts (many parts mean few rows: 55
+// parts of 32 rows took 15 us by one warp a row).
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int CL = D / 32;
+  constexpr int CL = D / 32, NW = WIDE ? 4 : 1;
+  __shared__ float sm_l[NW], sm_a[NW][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
+  const int w = WIDE ? warp : 0;
+  const long long row = WIDE ? static_cast<long long>(blockIdx.x) : static_cast<long long>(blockIdx.x) * 4 + warp;
   const long long rows = static_cast<long long>(p.rows.T) * p.Hq;
   if (row >= rows) return;
   const int tok = static_cast<int>(row / p.Hq);
@@ -465,12 +469,25 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const float z = m == neg_inf() ? 0.f : m;
   float l = 0.f, acc[CL] = {};
 #pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
+  for (int s = w; s < parts; s += NW) {
     const float f = fast_exp2(p.part_lse[s * rows + row] - z);
     const float* o = p.part_o + (s * rows + row) * D + lane * CL;
     l += f;
 #pragma unroll
     for (int c = 0; c < CL; ++c) acc[c] = fmaf(f, o[c], acc[c]);
+  }
+  if (WIDE) {
+    if (lane == 0) sm_l[w] = l;
+#pragma unroll
+    for (int c = 0; c < CL; ++c) sm_a[w][lane * CL + c] = acc[c];
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int y = 1; y < NW; ++y) {
+      l += sm_l[y];
+#pragma unroll
+      for (int c = 0; c < CL; ++c) acc[c] += sm_a[y][lane * CL + c];
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll

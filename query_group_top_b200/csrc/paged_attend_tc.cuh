@@ -409,8 +409,8 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const int r = (warp & 3) * 32 + lane;                   // row of the tile = TMEM lane
     // both query tiles into shared memory in the swizzled layout: a thread takes
     // one 16-byte piece of every RS-th row (rows behind the last repeat it: they
-    // go nowhere), eight loads in flight
-    constexpr int CH = D / 8, RS = 256 / CH, STEP = 8;
+    // go nowhere), all of its loads in flight
+    constexpr int CH = D / 8, RS = 256 / CH, STEP = CH;
     {
       const int ch = tid % CH, row0 = tid / CH;
       int tok = (r0 + row0) / p.grp, rem = (r0 + row0) % p.grp;   // of the packed row at hand
