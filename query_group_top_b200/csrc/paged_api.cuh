@@ -85,7 +85,7 @@ int run_rope(RopeParams rp, int dtype, const pivot_rope_t* rope, int d, cudaStre
   if (int rc = device_info(&dev)) return rc;
   rp.status = dev->status;
   // Tokens a block: its groups of d/16 lanes are dealt out to them, so that each
-  // group finds some eight rows at its token.  Fewer tokens a block where
+  // group finds some eight rows of a kind at its token.  Fewer tokens a block where
   // there are not enough for two blocks an SM: then latency counts, and a token's
   // heads go to as many groups as there are.
   const int most = std::max(rp.q.n, std::max(rp.k.n, rp.v.n)), groups = kRopeNT / (d / 16);

@@ -51,7 +51,7 @@ struct RopeParams {
   int* status;
 };
 
-constexpr int kRopeNT = 256;
+constexpr int kRopeNT = 128;
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -110,7 +110,7 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, const float* f) {
 
 // T: type of x and the weights; HALF: channel pairs (i, i + rot/2), else (2i, 2i+1).
 template <int D, bool HALF, class T>
-__global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 4 : 3) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeNT, 8) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LG = D / 16;              // lanes a head row
   constexpr int GROUPS = kRopeNT / LG;
   extern __shared__ float2 cs[];          // [tokens][rot / 2]
