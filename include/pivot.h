@@ -255,8 +255,8 @@ int pivot_qk_rope(const pivot_heads_t* q, const pivot_heads_t* k, int dtype, con
 /*
  * Writes the new keys (normed and rotated as above, at their rows' positions)
  * and values (NULL: a cache of keys alone) into their pages, and, where q is
- * given, norms and rotates the tokens' queries into out_q (bf16 [T][heads][d])
- * in the same launch.  The new tokens' rows must be in pages of their own: two
+ * given, norms and rotates the tokens' queries into out_q (bf16 [T][heads][d],
+ * contiguous; it may be q itself, as above) in the same launch.  The new tokens' rows must be in pages of their own: two
  * sequences that write the same row race.  A skipped sequence's rows and queries
  * are left as they were.
  */
@@ -279,7 +279,8 @@ typedef struct {
  *     out = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
  * over the keys that the query sees; a query that sees none, and every query of
  * a skipped sequence, gets zeros and lse = -inf.
- * q, out: bf16 [T][Hq][d]; out_lse: float32 [T][Hq] or NULL.  options NULL:
+ * q, out: bf16 [T][Hq][d], apart from one another; out_lse: float32 [T][Hq] or
+ * NULL.  options NULL:
  * scale d^-1/2, include_self.  max_seqlen: an upper bound on seqlens[b]; a
  * longer sequence is skipped.  Keys and values that a query does not see may
  * hold anything.  workspace as in the _ws variants; the size may be 0.

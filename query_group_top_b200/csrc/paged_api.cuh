@@ -118,14 +118,17 @@ struct PartCost {
   double per_key, fixed, join, join_per_part;
 };
 int best_parts(long long units, long long slots, long long len, const PartCost& c, long long most) {
-  most = std::min(most, std::max(1ll, 8 * slots / units));
   long long best = 1;
   double least = -1;
-  for (long long n = 1; n <= most; ++n) {
+  // the least is at one part or at the most parts of some number of rounds
+  for (long long r = 0; r <= 16; ++r) {
+    const long long n = r == 0 ? 1 : std::min(most, r * slots / units);
+    if (n < 1) continue;
     const double cost = static_cast<double>((units * n + slots - 1) / slots) *
                             (static_cast<double>((len + n - 1) / n) * c.per_key + c.fixed) +
                         (n > 1 ? c.join + static_cast<double>(n) * c.join_per_part : 0.0);
     if (least < 0 || cost < least) least = cost, best = n;
+    if (n == most && r > 0) break;
   }
   return static_cast<int>(best);
 }
@@ -296,6 +299,7 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
                           int Hq, int Hk, int d, int g, int num_pages, int page_size, int max_pages, int max_seqlen,
                           void* out, float* out_lse, void* workspace, size_t workspace_bytes, void* stream) {
   if (!q || !kpages || !vpages || !out) return fail(PIVOT_ERR_INVALID_ARG, "null tensor pointer");
+  if (out == q) return fail(PIVOT_ERR_INVALID_ARG, "out must not be q");
   if (!aligned16(q) || !aligned16(kpages) || !aligned16(vpages) || !aligned16(out))
     return fail(PIVOT_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   if (d != 64 && d != 128) return fail(PIVOT_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);

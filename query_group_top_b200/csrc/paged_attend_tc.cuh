@@ -20,13 +20,16 @@
 // While one tile's softmax runs, the tensor cores work for the other.  TMEM:
 // S_0, S_1 (128 columns each), O_0, O_1 (d each).
 //
-// O is rescaled only when a row's maximum has grown by more than 2^8 since the
-// last time (the row's reference stays behind its maximum, the weights then
-// reach up to 2^8, which fp32 sums and bf16 weights hold as exactly as those up
-// to 1); after the first tiles this hardly ever happens, and the four passes of
-// O through the registers are saved.  The score tile's commit also tells that
-// the earlier P V product is done (one thread issues both), so the softmax
-// warps may change O between it and their own arrival.
+// O is rescaled only when a row's maximum has grown by more than 2^40 since the
+// last time.  Until then the row's reference stays behind its maximum and the
+// weights reach up to 2^40, which fp32 sums and bf16 weights hold as exactly as
+// those up to 1 (their sums stay below 2^127 for any length, and a value that
+// were to overflow them ends in the row by row form).  With keys of uneven
+// length some row of a warp grows by 2^8 in most early tiles: rescaling at that
+// took 279 us for 264 (8192-token prefill, 16 heads, 1 % of the keys four times
+// as long).  The score tile's commit also tells that the earlier P V product is done
+// (one thread issues both), so the softmax warps may change O between it and
+// their own arrival.
 #pragma once
 
 #include "paged_attend.cuh"
@@ -53,7 +56,7 @@ struct TcCfg {
   static_assert(SMEM > 116 * 1024, "one CTA an SM: each takes the whole TMEM");
 };
 
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kRescaleLog2 = 40.f;
 // Of 16 pairs of weights, how many exp2_poly makes.  At 64 channels the special
 // functions bound the loop (half the products for as many weights): 3 of 16
 // took 178 us for 197 (4 chunks of 2048 tokens, 16 heads, contexts of 2048);

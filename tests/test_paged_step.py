@@ -82,12 +82,15 @@ def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
     assert append(d=96) == 2
 
     def attend(q=ptr, kp=ptr, vp=ptr, bt=ptr, sl=ptr, cu=None, opt=None, T=4, B=2, Hq=4, Hk=2, d=128, g=2, n=8, page=16,
-               mp=4, ms=64, out=ptr, ws=None, nb=0):
+               mp=4, ms=64, out=None, ws=None, nb=0):
+        out = ptr + 32 if out is None else out
         return lib.pivot_paged_attention(q, kp, vp, bt, sl, cu, opt, T, B, Hq, Hk, d, g,
                                          n, page, mp, ms, out, None, ws, nb, None)
 
-    assert attend(q=None) == 1 and attend(out=None) == 1 and attend(kp=None) == 1 and attend(vp=None) == 1
+    assert attend(q=None) == 1 and attend(out=0) == 1 and attend(kp=None) == 1 and attend(vp=None) == 1
     assert attend(q=ptr + 4) == 1
+    assert attend(out=ptr + 32) == 2 if not torch.cuda.is_available() else True    # right otherwise: no device
+    assert attend(out=ptr) == 1 and b"out must not be q" in lib.pivot_last_error()
     assert attend(Hq=3) == 1 and attend(Hk=0) == 1 and attend(Hq=1) == 1
     assert attend(d=80) == 2
     assert attend(T=3) == 1 and attend(g=0) == 1
@@ -151,6 +154,22 @@ def test_spans_and_pages_that_do_not_fit_are_refused(rows_lib):
     # a cache row behind 32 bits
     far = (ctypes.c_int * 1)(2000000000)
     assert rows_lib.row(far, 1, 2147483647, 8, 0, 255) == 2000000000 * 256 + 255
+
+
+def test_option_structs_are_packed_as_the_header_lays_them_out(tmp_path):
+    src = tmp_path / "sizes.c"
+    src.write_text('#include "pivot.h"\n#include <stdio.h>\n#include <string.h>\nint main(void) {\n'
+                   '  pivot_heads_t h; pivot_rope_t r; pivot_attend_t a;\n'
+                   '  memset(&h, 0, sizeof h); memset(&r, 0, sizeof r); memset(&a, 0, sizeof a);\n'
+                   '  h.data = (void*)1; h.weight = (void*)2; h.token_stride = 3; h.head_stride = -4; h.heads = 5;\n'
+                   '  r.freqs = (double*)6; r.amplitude = 0.5; r.eps = 0.25; r.rot_dim = 7; r.layout = 8;\n'
+                   '  a.scale = 0.125; a.include_self = 9;\n'
+                   '  fwrite(&h, sizeof h, 1, stdout); fwrite(&r, sizeof r, 1, stdout); fwrite(&a, sizeof a, 1, stdout);\n'
+                   '  return 0;\n}\n')
+    exe = tmp_path / "sizes"
+    subprocess.check_call(["gcc", "-I", os.path.join(ROOT, "include"), "-o", str(exe), str(src)])
+    want = qg._HEADS(1, 2, 3, -4, 5) + qg._ROPE(6, 0.5, 0.25, 7, 8) + qg._ATTEND(0.125, 9)
+    assert subprocess.check_output([str(exe)]) == want
 
 
 def test_rope_frequencies():
@@ -508,6 +527,62 @@ def test_paged_attention_many_sequences_one_long():
     check_attention(c, q, out, lse, True, 0.125)
 
 
+@gpu
+@pytest.mark.parametrize("page", [2, 16])
+def test_paged_attention_waits_run_out_and_the_next_call_is_exact(page):
+    """The waits of the matrix-tile kernels are bounded: under a limit of a nanosecond a call either gives up and says
+    so (a wait that is over at its first look does not) or is right, and leaves the device as it was."""
+    c = ref.Cache([9000], [64], 2, 128, page, seed=17)
+    q = normal((64, 4, 128), 65)
+    want, lse = attend(c, q, True, True)
+    assert qg.sync_status() == 0
+    lib = qg.load_library()
+    told = 0
+    try:
+        lib.pivot_set_wait_limit(1)
+        for _ in range(20):
+            out, _ = attend(c, q, True, True)
+            try:
+                assert qg.sync_status() == 0
+                assert same_bits(out, want)
+            except qg.PivotError as e:
+                assert "timed out" in str(e)
+                told += 1
+    finally:
+        lib.pivot_set_wait_limit(0)
+    again, lse2 = attend(c, q, True, True)
+    assert qg.sync_status() == 0
+    assert same_bits(again, want) and same_bits(lse, lse2)
+    print(f"{told} of 20 calls gave up")
+
+
+@gpu
+@pytest.mark.parametrize("page", [1, 16])
+def test_rows_behind_two_to_the_thirty_one_elements(page):
+    """A cache whose last pages lie behind 2^31 elements (2^32 bytes): append, both attentions and the index rows
+    address them."""
+    H, d, held, g = 4, 128, 300, 2
+    near = ref.Cache([held], [g], H, d, page, seed=19, fill=0.0)
+    total = (1 << 31) // (page * H * d) + 64 + near.kpages.shape[0]
+    kp = torch.empty((total, page, H, d), dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    shift = total - near.kpages.shape[0]
+    kp[shift:], vp[shift:] = near.kpages, near.vpages
+    table = torch.where(near.table >= 0, near.table + shift, near.table)
+    f, _ = qg.rope_frequencies(d)
+    k, v = normal((1, g, H, d), 66), normal((1, g, H, d), 67)
+    qg.paged_append(k, v, kp, vp, table, near.seqlens, freqs=f)
+    qg.paged_append(k, v, near.kpages, near.vpages, near.table, near.seqlens, freqs=f)
+    assert same_bits(kp[shift:], near.kpages) and same_bits(vp[shift:], near.vpages)
+    q = normal((1, g, H, d), 68)
+    idx = torch.arange(250, dtype=torch.int32, device="cuda").expand(1, g, H, 250).contiguous()
+    for call in (lambda a, b, t: qg.paged_attention(q, a, b, t, near.seqlens, held + g),
+                 lambda a, b, t: qg.paged_attention(normal((1, g, 32 * H, d), 69), a, b, t, near.seqlens, held + g),
+                 lambda a, b, t: qg.sparse_attention_paged(q, a, b, t, near.seqlens, idx)):
+        assert same_bits(call(kp, vp, table), call(near.kpages, near.vpages, near.table))
+    assert qg.sync_status() == 0
+
+
 # ------------------------------------------------------------------ attention over index rows
 @gpu
 @pytest.mark.parametrize("page", [1, 16, 128])
@@ -692,6 +767,7 @@ def test_the_binding_refuses():
     no(lambda: A(m=0))
     no(lambda: A(scale=0.0))
     no(lambda: A(out=torch.empty_like(q.float())))
+    no(lambda: A(out=q))
     no(lambda: A(out_lse=torch.empty((4, 4), device="cuda")))
     P = lambda k=k, v=k, kp=c.kpages, vp=c.vpages, **kw: qg.paged_append(k, v, kp, vp, c.table, c.seqlens, **{"freqs": f, **kw})  # noqa: E731
     no(lambda: P(v=None))
