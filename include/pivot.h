@@ -282,7 +282,8 @@ typedef struct {
  * q, out: bf16 [T][Hq][d], apart from one another; out_lse: float32 [T][Hq] or
  * NULL.  options NULL:
  * scale d^-1/2, include_self.  max_seqlen: an upper bound on seqlens[b]; a
- * longer sequence is skipped.  Keys and values that a query does not see may
+ * longer sequence is skipped.  With cu_q, g is an upper bound on a sequence's new
+ * tokens, for the choice of kernels alone, or 0.  Keys and values that a query does not see may
  * hold anything.  workspace as in the _ws variants; the size may be 0.
  */
 size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int max_seqlen);

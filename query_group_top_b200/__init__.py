@@ -623,14 +623,15 @@ def paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new=None, freqs=
 
 
 def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=None, scale=None, include_self=True,
-                    out=None, out_lse=None, stream=None):
+                    out=None, out_lse=None, stream=None, max_q=None):
     """Dense causal attention of new tokens over the paged cache that holds their keys and values already.
 
     q: bf16 [B, g, Hq, d] (a decode step), or [T, Hq, d] with cu_q int32 [B + 1] (chunks of any lengths; rows of
     tokens behind cu_q[B] are left as they were); Hq a multiple of the cache's heads, query head h reads key head
     h // (Hq // Hk).  Token i of n_b sits at position seqlens[b] - n_b + i and sees the keys up to its own, or, with
     include_self=False, those before it (the indexer's keys); a query that sees none gets zeros and lse -inf.
-    max_seqlen bounds seqlens.  scale: d ** -0.5 by default.  out_lse: float32 [..., Hq], the log of each row's sum.
+    max_seqlen bounds seqlens; max_q (with cu_q, optional) bounds a sequence's new tokens, which spares a batch of
+    single tokens the launch for longer ones.  scale: d ** -0.5 by default.  out_lse: float32 [..., Hq], the log of each row's sum.
     Returns bf16 with q's shape."""
     lib = _lib or load_library()
     sh, dev = _tokens("q", q)
@@ -642,6 +643,10 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
         raise PivotError(f"q's heads must be a multiple of the cache's {Hk} (got {Hq})")
     T, B, g, max_pages, pcu, psl, pbt = _sequences(sh, cu_q, seqlens, block_table, dev, "cu_q")
     max_seqlen = int(max_seqlen)
+    if max_q is not None and cu_q is not None:
+        if max_q < 1:
+            raise PivotError("max_q must be >= 1")
+        g = int(max_q)
     opt = _ATTEND(d ** -0.5 if scale is None else scale, 1 if include_self else 0)
     with _On(dev, stream, (q, kpages, vpages, block_table, seqlens, cu_q, out, out_lse)) as raw:
         out = _like(out, q, torch.bfloat16, "out")

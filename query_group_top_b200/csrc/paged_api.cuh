@@ -138,13 +138,18 @@ struct AttendPlan {
   bool tiles;               // attend_tiles_kernel, else attend_rows_kernel
   int rows;                 // packed rows of a CTA
   int nsplit, min_chunk;
+  int nsplit_many;          // of the sequences of many rows among those of few
   size_t part_lse, total;   // workspace: the parts' rows at 0, their lse at part_lse
 };
+
+constexpr int kFewRows = 16;   // packed rows of a sequence up to which attend_rows_kernel takes it
 
 AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int sms) {
   AttendPlan a{};
   const long long rows = static_cast<long long>(T) * (Hq / Hk);
-  a.tiles = rows >= 32ll * B;
+  // At 16 rows a sequence the two take the same (two sequences of 32000, 8 key
+  // heads: 56 us), at 24 the matrix tiles 34 us for 61 (16 sequences of 2000).
+  a.tiles = rows > static_cast<long long>(kFewRows) * B;
   a.rows = a.tiles ? 256 : rows <= 8ll * B ? 8 : 16;
   a.min_chunk = 256;
   const long long ctas = B * ((rows + static_cast<long long>(B) * a.rows - 1) / (static_cast<long long>(B) * a.rows)) * Hk;
@@ -159,6 +164,9 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int 
     a.nsplit = best_parts(ctas, static_cast<long long>(per_sm) * sms, max_seqlen,
                           PartCost{4. * d / 41. * per_sm, 3300, 4500, part_bytes / 5000}, most);
   }
+  // the matrix tiles' launch for long chunks among single tokens, which may find
+  // none: two parts at most, so that it is over soon
+  a.nsplit_many = a.tiles ? a.nsplit : std::min(a.nsplit, 2);
   if (a.nsplit > 1) {
     const size_t parts = static_cast<size_t>(a.nsplit) * T * Hq;
     a.part_lse = up(parts * d * sizeof(float));
@@ -168,8 +176,11 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int 
 }
 
 template <int D>
-int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(static_cast<long long>(ap.tiles) * ap.Hk * ap.nsplit);
+int launch_attend_kernel(PagedAttendParams ap, bool tiles, int rows_per_cta, long long row_tiles, cudaStream_t st) {
+  const long long ctas = row_tiles * ap.Hk * (tiles ? ap.nsplit_many : ap.nsplit);
+  if (ctas >= (1ll << 31)) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
+  ap.tiles = static_cast<int>(row_tiles);
+  const unsigned grid = static_cast<unsigned>(ctas);
   if (tiles) {
     CUtensorMap mk{}, mv{};
     TraceScope tr("attend_tiles", st);
@@ -194,6 +205,33 @@ int launch_attend(const PagedAttendParams& ap, bool tiles, int rows_per_cta, cud
     }
   }
   CUDA_TRY(cudaGetLastError());
+  return PIVOT_OK;
+}
+
+// most_new: with cu, a bound on a sequence's new tokens, 0 unknown.
+template <int D>
+int launch_attend(PagedAttendParams ap, const AttendPlan& pl, int most_new, cudaStream_t st) {
+  const long long packed = static_cast<long long>(ap.rows.T) * ap.grp, B = ap.rows.B;
+  ap.over = 0;
+  ap.upto = 0x7FFFFFFF;
+  ap.many = pl.tiles ? -1 : 0x7FFFFFFF;   // one kernel takes every sequence
+  if (!ap.rows.cu) {
+    const long long per = (static_cast<long long>(ap.rows.g) * ap.grp + pl.rows - 1) / pl.rows;
+    if (int rc = launch_attend_kernel<D>(ap, pl.tiles, pl.rows, B * per, st)) return rc;
+  } else {
+    // Few rows a sequence on average may still be one long chunk among many
+    // single tokens: then the sequences are dealt out by their own rows, and
+    // those of many go to the matrix tiles (a chunk of 512 tokens among 200
+    // single ones over 4000 keys, 32 heads over 8: 632 us for 822; where there
+    // is none, the launch costs some 4 us, which a bound on the tokens spares).
+    if (!pl.tiles && packed > kFewRows && (most_new == 0 || static_cast<long long>(most_new) * ap.grp > kFewRows)) {
+      ap.over = ap.many = kFewRows;
+      if (int rc = launch_attend_kernel<D>(ap, true, 256, packed / 256 + std::min(B, packed / (kFewRows + 1)), st)) return rc;
+      ap.over = 0;
+      ap.upto = kFewRows;
+    }
+    if (int rc = launch_attend_kernel<D>(ap, pl.tiles, pl.rows, (packed + pl.rows - 1) / pl.rows + B, st)) return rc;
+  }
   if (ap.nsplit > 1) {
     TraceScope tr("attend_join", st);
     cudaLaunchConfig_t cfg{};
@@ -308,6 +346,7 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   PagedAttendParams ap{};
   if (int rc = paged_rows(block_table, seqlens, cu_q, T, B, g, num_pages, page_size, max_pages, max_seqlen, &ap.rows))
     return rc;
+  if (cu_q && g < 0) return fail(PIVOT_ERR_INVALID_ARG, "with cu_q, g bounds a sequence's new tokens (0: unknown)");
   if (max_seqlen >= (1 << 30)) return fail(PIVOT_ERR_INVALID_ARG, "max_seqlen too large");
   const double scale = options ? options->scale : 1.0 / sqrt(static_cast<double>(d));
   if (!(scale > 0.0) || !(scale < 1e30)) return fail(PIVOT_ERR_INVALID_ARG, "scale must be positive and finite");
@@ -327,20 +366,17 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   ap.grp = Hq / Hk;
   ap.self_key = options ? (options->include_self != 0) : 1;
   ap.nsplit = pl.nsplit;
+  ap.nsplit_many = pl.nsplit_many;
   ap.min_chunk = pl.min_chunk;
-  const long long tiles = cu_q ? (static_cast<long long>(T) * ap.grp + pl.rows - 1) / pl.rows + B
-                               : B * ((static_cast<long long>(g) * ap.grp + pl.rows - 1) / pl.rows);
-  if (tiles * Hk * pl.nsplit >= (1ll << 31)) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
-  ap.tiles = static_cast<int>(tiles);
   ap.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
   ap.out = static_cast<uint16_t*>(out);
   ap.lse = out_lse;
-  ap.part_o = static_cast<float*>(workspace);
+  ap.part_o = pl.total ? static_cast<float*>(workspace) : nullptr;
   ap.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.part_lse);
   ap.status = dev->status;
   ap.wait_ns = wait_limit_ns();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_attend<128>(ap, pl.tiles, pl.rows, st) : launch_attend<64>(ap, pl.tiles, pl.rows, st);
+  return d == 128 ? launch_attend<128>(ap, pl, g, st) : launch_attend<64>(ap, pl, g, st);
 }
 
 int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,

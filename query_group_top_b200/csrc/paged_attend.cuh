@@ -11,7 +11,7 @@
 //
 // The query heads of one key head are packed as rows (row r is token r / grp,
 // head r % grp of the group), so one read of a key serves them all.  A long
-// axis is split: each CTA takes chunk_of(len) keys, and attend_join_kernel adds up
+// axis is split: each CTA takes chunk_of(sequence) keys, and attend_join_kernel adds up
 // the parts, o = sum_c w_c o_c, w_c = exp(lse_c - lse).
 //
 // attend_rows_kernel is the form for few rows per key head (decode), bound by
@@ -40,21 +40,24 @@ struct PagedAttendParams {
   int self_key;            // 1: a query sees its own key
   int nsplit, min_chunk;   // CTAs along the keys of each row tile; the fewest keys that a part is worth
   int tiles;               // row tiles over all sequences (an upper bound where cu is given)
+  int over, upto;          // with cu: the packed rows of the sequences that this launch takes, over < rows <= upto
+  int many, nsplit_many;   // sequences of more packed rows than `many` are cut into nsplit_many parts, not nsplit
   float scale_log2;        // scale * log2(e)
   uint16_t* out;           // [T][Hq][d] bf16
   float* lse;              // [T][Hq] natural log, or null
-  float* part_o;           // nsplit > 1: [nsplit][T][Hq][d], each part normalised
-  float* part_lse;         // nsplit > 1: [nsplit][T][Hq], log2 units
+  float* part_o;           // where keys are split: [parts][T][Hq][d], each part normalised; else null
+  float* part_lse;         // [parts][T][Hq], log2 units
   int* status;
   unsigned long long wait_ns;
 };
 
 constexpr float kLn2 = 0.693147180559945309f;
 
-// Keys per part of a sequence of `len` rows: an nsplit-th of it, whatever the
-// bound that sized the grid, in whole 128-key tiles, and no less than min_chunk.
-__device__ __forceinline__ int chunk_of(int len, const PagedAttendParams& p) {
-  return max(p.min_chunk, ((len + p.nsplit - 1) / p.nsplit + 127) & ~127);
+// Keys per part of a sequence: an nsplit-th of its rows, whatever the bound that
+// sized the grid, in whole 128-key tiles, and no less than min_chunk.
+__device__ __forceinline__ int chunk_of(const NewSpan& sp, const PagedAttendParams& p) {
+  const int parts = sp.n * p.grp > p.many ? p.nsplit_many : p.nsplit;
+  return max(p.min_chunk, ((sp.len + parts - 1) / parts + 127) & ~127);
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -66,12 +69,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 // The row tile `flat` of the batch: which sequence, and which of its tiles of
 // `rows` packed rows.  One warp; without cu every sequence has the same number
-// of tiles, else the sequences' tile counts are summed 32 at a time.  Returns
-// -1 behind the last tile.
-__device__ __forceinline__ int locate_tile(const PagedRows& p, int grp, int rows, int flat, int lane, int* tile,
-                                           int* status) {
+// of tiles, else the tile counts of the sequences that the launch takes are
+// summed 32 at a time.  Returns -1 behind the last tile.
+__device__ __forceinline__ int locate_tile(const PagedAttendParams& a, int rows, int flat, int lane, int* tile) {
+  const PagedRows& p = a.rows;
   if (!p.cu) {
-    const int per = (p.g * grp + rows - 1) / rows;
+    const int per = (p.g * a.grp + rows - 1) / rows;
     *tile = flat % per;
     return flat / per < p.B ? flat / per : -1;
   }
@@ -81,8 +84,9 @@ __device__ __forceinline__ int locate_tile(const PagedRows& p, int grp, int rows
     int n = 0;
     if (b < p.B) {
       const NewSpan sp = p.span(b);
-      n = static_cast<int>((static_cast<long long>(sp.n) * grp + rows - 1) / rows);
-      if (!sp.ok) atomicOr(status, kStBadLen);
+      const int packed = sp.n * a.grp;
+      if (packed > a.over && packed <= a.upto) n = static_cast<int>((static_cast<long long>(packed) + rows - 1) / rows);
+      if (!sp.ok) atomicOr(a.status, kStBadLen);
     }
     int sum = n;
 #pragma unroll
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
   const int flat = static_cast<int>(bid / p.Hk / p.nsplit);
   if (warp == 0) {
     int tile = 0;
-    const int b = locate_tile(p.rows, p.grp, ROWS, flat, lane, &tile, p.status);
+    const int b = locate_tile(p, ROWS, flat, lane, &tile);
     if (lane == 0) seq_s[0] = b, seq_s[1] = tile;
   }
   __syncthreads();
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
     return (static_cast<long long>(sp.tok0) + (r0 + r) / p.grp) * p.Hq + hk * p.grp + (r0 + r) % p.grp;
   };
   if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
-  const int chunk = chunk_of(sp.len, p);
+  const int chunk = chunk_of(sp, p);
   const int kbeg = split * chunk;
   const int kend = min(lim_of(nrows - 1), kbeg + chunk);
   if (kbeg >= kend && split > 0) return;                   // the join reads no part a row has no keys in
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
     const long long row = row_of(r);
     if (!__all_sync(0xffffffffu, fine))
       attend_row_exact<D>(p, b, hk, row, kbeg, min(kend, lim_of(r)), lane, acc, &lse2);
-    if (p.nsplit > 1) {
+    if (p.part_o) {
       const long long at = static_cast<long long>(split) * p.rows.T * p.Hq + row;
 #pragma unroll
       for (int c = 0; c < CL; ++c) p.part_o[at * D + lane * CL + c] = acc[c];
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
 
 // ------------------------------------------------------------------ joining the parts
 // The parts that hold keys of the row are the first
-// ceil(lim / chunk_of(len)) (at least one), whichever kernel wrote them.  Launched
+// ceil(lim / chunk_of(sequence)) (at least one), whichever kernel wrote them.  Launched
 // while that kernel still runs, it looks its row up and then waits for it.
 // WIDE: a CTA's four warps share a row's parts (many parts mean few rows: 55
 // parts of 32 rows took 15 us by one warp a row).
@@ -459,7 +463,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const NewSpan sp = p.rows.span(find_sequence(p.rows, tok, lane));
   if (tok < sp.tok0 || tok >= sp.tok0 + sp.n) return;
   const int lim = sp.ok ? sp.len - sp.n + p.self_key + (tok - sp.tok0) : 0;
-  const int chunk = chunk_of(sp.len, p);
+  const int chunk = chunk_of(sp, p);
   const int parts = max(1, (lim + chunk - 1) / chunk);
   grid_wait();
   float m = neg_inf();

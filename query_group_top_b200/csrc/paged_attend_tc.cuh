@@ -119,11 +119,11 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   // key heads innermost (neighbouring CTAs share pages), the longest row tiles first
   const unsigned bid = blockIdx.x;
   const int hk = static_cast<int>(bid % p.Hk);
-  const int split = static_cast<int>(bid / p.Hk % p.nsplit);
-  const int flat = p.tiles - 1 - static_cast<int>(bid / p.Hk / p.nsplit);
+  const int split = static_cast<int>(bid / p.Hk % p.nsplit_many);
+  const int flat = p.tiles - 1 - static_cast<int>(bid / p.Hk / p.nsplit_many);
   if (warp == 0) {
     int tile = 0;
-    const int b = locate_tile(p.rows, p.grp, 2 * C::BM, flat, lane, &tile, p.status);
+    const int b = locate_tile(p, 2 * C::BM, flat, lane, &tile);
     if (lane == 0) {
       seq_s[0] = b;
       seq_s[1] = tile;
@@ -153,7 +153,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
   const int pos0 = sp.len - sp.n + p.self_key;
   auto lim_of = [&](int r) { return sp.ok ? pos0 + r / p.grp : 0; };
-  const int chunk = chunk_of(sp.len, p);
+  const int chunk = chunk_of(sp, p);
   const int kbeg = split * chunk;
   // keys of the part that the last row of tile t sees; its key tiles
   int kend[2], nk[2];
@@ -560,7 +560,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           fine = fine && fabsf(f[x]) < __int_as_float(0x7f800000);
         }
         if (!row_ok) continue;
-        if (p.nsplit > 1) {
+        if (p.part_o) {
 #pragma unroll
           for (int x = 0; x < 32; x += 4)
             *reinterpret_cast<float4*>(p.part_o + at * D + 32 * c + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
@@ -570,7 +570,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
       }
       if (row_ok) {
-        if (p.nsplit > 1)
+        if (p.part_o)
           p.part_lse[at] = lse2;
         else if (p.lse)
           p.lse[row] = lse2 * kLn2;
@@ -582,7 +582,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const int lx = __shfl_sync(0xffffffffu, lim, x);
         float o[D / 32], z;
         attend_row_exact<D>(p, b, hk, rx, kbeg, min(lx, kbeg + chunk), lane, o, &z);
-        if (p.nsplit > 1) {
+        if (p.part_o) {
           const long long ax = static_cast<long long>(split) * p.rows.T * p.Hq + rx;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) p.part_o[ax * D + lane * (D / 32) + c] = o[c];

@@ -528,6 +528,32 @@ def test_paged_attention_many_sequences_one_long():
 
 
 @gpu
+@pytest.mark.parametrize("held0", [40, 3000])
+@pytest.mark.parametrize("page,d", [(16, 128), (1, 64)])
+def test_paged_attention_chunks_among_single_tokens(page, d, held0):
+    """A few rows a sequence on average, but some with many: those go to the matrix tiles, the others do not, whatever
+    bound on the new tokens is given, and bad lengths among them are told."""
+    new = [1] * 20 + [90] + [1] * 25 + [0, 2, 9, 1] + [1] * 14
+    held = [(held0 + 37 * i) % (held0 + 50) for i in range(len(new))]
+    c = ref.Cache(held, new, 2, d, page, seed=23)
+    q = normal((sum(new), 4, d), 63)
+    out, lse = attend(c, q, True, True)
+    assert qg.sync_status() == 0
+    check_attention(c, q, out, lse, True, d ** -0.5)
+    for bound in (1, 90, 4000):     # 1 is wrong: the choice of kernels follows it, the result does not
+        got, lse2 = attend(c, q, True, True, max_q=bound)
+        assert qg.sync_status() == 0
+        check_attention(c, q, got, lse2, True, d ** -0.5, f"bound {bound}")
+    lens = c.seqlens.clone()
+    lens[20], lens[47] = 3, 1       # fewer rows than new tokens
+    c.seqlens = lens
+    bad, _ = attend(c, q, True, True)
+    with pytest.raises(qg.PivotError):
+        qg.sync_status()
+    assert same_bits(bad[:20], out[:20]) and bool((bad[20:110] == 0).all()) and same_bits(bad[110:135], out[110:135])
+
+
+@gpu
 @pytest.mark.parametrize("page", [2, 16])
 def test_paged_attention_waits_run_out_and_the_next_call_is_exact(page):
     """The waits of the matrix-tile kernels are bounded: under a limit of a nanosecond a call either gives up and says
@@ -765,6 +791,7 @@ def test_the_binding_refuses():
     no(lambda: A(kp=c.kpages[:, :12].contiguous(), vp=c.vpages[:, :12].contiguous()))
     no(lambda: A(vp=c.vpages[:-1]))
     no(lambda: A(m=0))
+    no(lambda: A(q=q.view(4, 4, 64), cu_q=c.cu, max_q=0))
     no(lambda: A(scale=0.0))
     no(lambda: A(out=torch.empty_like(q.float())))
     no(lambda: A(out=q))
