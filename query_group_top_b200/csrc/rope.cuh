@@ -19,7 +19,11 @@
 // head row, 16 channels a lane in 16-byte loads, the pair's two halves in the
 // same lane, so that the only exchange is the norm's sum over those lanes; they
 // stay with their token, whose cosines they hold in registers, and walk its
-// heads, so that the next row's address is one addition away.
+// heads, so that the next row's address is one addition away and its loads run
+// ahead of the arithmetic.  Blocks of 128 threads, seven an SM: 8192 tokens of
+// 32 heads of 128, normed and turned, take 30 us, a plain copy of the same bytes
+// 25; 27 of them are the kernel without norm and rotation.  32768 tokens of 40
+// heads: 123 us, the copy 113.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -110,12 +114,13 @@ __device__ __forceinline__ void store8_bf16(uint16_t* p, const float* f) {
 
 // T: type of x and the weights; HALF: channel pairs (i, i + rot/2), else (2i, 2i+1).
 template <int D, bool HALF, class T>
-__global__ void __launch_bounds__(kRopeNT, 8) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 7 : 6) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LG = D / 16;              // lanes a head row
   constexpr int GROUPS = kRopeNT / LG;
   extern __shared__ float2 cs[];          // [tokens][rot / 2]
   __shared__ int pos_s[GROUPS];
   __shared__ long long row_s[GROUPS];     // cache row of the token; -1: leave the token out
+  __shared__ float4 w_s[2][4][LG];        // norm weights of q and k, a lane's 16 in four pieces
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tb = p.tokens_per_block, gpt = GROUPS / tb;   // groups a token
@@ -132,19 +137,36 @@ __global__ void __launch_bounds__(kRopeNT, 8) rope_kernel(const __grid_constant_
 
   // A group walks rows g, g + gpt, ... of the token's queries, then keys, then
   // values, in rounds that are the same for all lanes of a warp (for the norm's
-  // shuffles); behind a kind's last row it repeats that row and drops the result.
-  // The next row is loaded before the one at hand is worked on.
-  const int rq = (p.q.n + gpt - 1) / gpt, rk = rq + (p.k.n + gpt - 1) / gpt, rounds = rk + (p.v.n + gpt - 1) / gpt;
+  // shuffles); behind a kind's last row it repeats its first and drops the
+  // result.  The next row is loaded before the one at hand is worked on.
+  auto first = [&](const HeadRows& src) {
+    return static_cast<const T*>(src.x) + t * src.token_stride + min(g, src.n - 1) * src.head_stride;
+  };
+  const T* const q0 = p.q.n ? first(p.q) : nullptr;
+  const T* const k0 = p.k.n ? first(p.k) : nullptr;
+  const T* const v0 = p.v.n ? first(p.v) : nullptr;
   Vec8<T> va, vb;
-  auto load = [&](int x) {
-    const HeadRows& src = x < rq ? p.q : x < rk ? p.k : p.v;
-    const int h = min(g + gpt * (x - (x < rq ? 0 : x < rk ? rq : rk)), src.n - 1);
-    const T* row = static_cast<const T*>(src.x) + t * src.token_stride + h * src.head_stride;
+  auto load = [&](const T* row) {
     va.load(row + ca);
     vb.load(row + cb);
   };
-  load(0);   // on its way while the positions and angles are worked out
+  load(q0 ? q0 : k0);   // on its way while the positions and angles are worked out
   const double freq0 = half ? p.freqs[threadIdx.x % half] : 0.0;
+  if (threadIdx.x < 2 * LG) {
+    const T* w = static_cast<const T*>(threadIdx.x < LG ? p.q.weight : p.k.weight);
+    if (w != nullptr) {
+      Vec8<T> wa, wb;
+      float f[16];
+      wa.load(w + ca);
+      wb.load(w + cb);
+      wa.get(f);
+      wb.get(f + 8);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)   // in the order of the register pairs below
+        w_s[threadIdx.x / LG][c][sub] = HALF ? make_float4(f[2 * c], f[2 * c + 1], f[8 + 2 * c], f[9 + 2 * c])
+                                             : make_float4(f[4 * c], f[4 * c + 2], f[4 * c + 1], f[4 * c + 3]);
+    }
+  }
 
   for (int i = warp; i < nt; i += kRopeNT / 32) {
     const int ti = t0 + i;
@@ -195,72 +217,74 @@ __global__ void __launch_bounds__(kRopeNT, 8) rope_kernel(const __grid_constant_
       si2[c] = pair_f32(x.y, y.y);
     }
   }
-  for (int x = 0; x < rounds; ++x) {
-    const int kind = x < rq ? 0 : x < rk ? 1 : 2;
-    const HeadRows& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-    const int h = g + gpt * (x - (kind == 0 ? 0 : kind == 1 ? rq : rk));
-    float f[16];
-    va.get(f);
-    vb.get(f + 8);
-    if (x + 1 < rounds) load(x + 1);
-    // channels in register pairs: those of a lane's a halves, then its b halves
-    uint64_t a[4], b[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      a[c] = HALF ? pair_f32(f[2 * c], f[2 * c + 1]) : pair_f32(f[4 * c], f[4 * c + 2]);
-      b[c] = HALF ? pair_f32(f[8 + 2 * c], f[9 + 2 * c]) : pair_f32(f[4 * c + 1], f[4 * c + 3]);
-    }
-    if (src.weight != nullptr) {
-      const T* w = static_cast<const T*>(src.weight);
-      float gw[16];
-      Vec8<T> wa, wb;
-      wa.load(w + ca);
-      wb.load(w + cb);
-      wa.get(gw);
-      wb.get(gw + 8);
-      uint64_t s2 = mul2(a[0], a[0]);
-#pragma unroll
-      for (int c = 1; c < 4; ++c) s2 = fma2(a[c], a[c], s2);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s2 = fma2(b[c], b[c], s2);
-      float lo, hi;
-      unpair_f32(s2, lo, hi);
-      float ss = lo + hi;
-#pragma unroll
-      for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      const uint64_t r2 = pair_f32(r, r);
+  // One kind's rows: src from row0 on, to dst + head * D; next: the first row of the kind behind it.
+  auto walk = [&](const HeadRows& src, const T* row0, uint16_t* dst, bool turn, const float4 (*w)[LG], const T* next) {
+    const long long step = gpt * src.head_stride;
+    const T* at = row0;
+    dst += g * D;
+    for (int h = g, left = (src.n + gpt - 1) / gpt; left > 0; --left, h += gpt, dst += gpt * D) {
+      float f[16];
+      va.get(f);
+      vb.get(f + 8);
+      at += step;
+      if (left > 1)
+        load(h + gpt < src.n ? at : row0);
+      else if (next)
+        load(next);
+      // channels in register pairs: those of a lane's a halves, then its b halves
+      uint64_t a[4], b[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        a[c] = mul2(mul2(a[c], r2), HALF ? pair_f32(gw[2 * c], gw[2 * c + 1]) : pair_f32(gw[4 * c], gw[4 * c + 2]));
-        b[c] = mul2(mul2(b[c], r2), HALF ? pair_f32(gw[8 + 2 * c], gw[9 + 2 * c]) : pair_f32(gw[4 * c + 1], gw[4 * c + 3]));
+        a[c] = HALF ? pair_f32(f[2 * c], f[2 * c + 1]) : pair_f32(f[4 * c], f[4 * c + 2]);
+        b[c] = HALF ? pair_f32(f[8 + 2 * c], f[9 + 2 * c]) : pair_f32(f[4 * c + 1], f[4 * c + 3]);
       }
-    }
-    if (turns && kind != 2) {
+      if (src.weight != nullptr) {
+        uint64_t s2 = mul2(a[0], a[0]);
+#pragma unroll
+        for (int c = 1; c < 4; ++c) s2 = fma2(a[c], a[c], s2);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s2 = fma2(b[c], b[c], s2);
+        float lo, hi;
+        unpair_f32(s2, lo, hi);
+        float ss = lo + hi;
+#pragma unroll
+        for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const uint64_t r2 = pair_f32(r, r);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 g4 = w[c][sub];
+          a[c] = mul2(mul2(a[c], r2), pair_f32(g4.x, g4.y));
+          b[c] = mul2(mul2(b[c], r2), pair_f32(g4.z, g4.w));
+        }
+      }
+      if (turn) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint64_t y = a[c], z = b[c];
+          a[c] = fma2(y, co2[c], mul2(z, si2[c] ^ 0x8000000080000000ull));   // the sines' signs turned
+          b[c] = fma2(y, si2[c], mul2(z, co2[c]));
+        }
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint64_t y = a[c], z = b[c];
-        a[c] = fma2(y, co2[c], mul2(z, si2[c] ^ 0x8000000080000000ull));   // the sines' signs turned
-        b[c] = fma2(y, si2[c], mul2(z, co2[c]));
+        if (HALF) {
+          unpair_f32(a[c], f[2 * c], f[2 * c + 1]);
+          unpair_f32(b[c], f[8 + 2 * c], f[9 + 2 * c]);
+        } else {
+          unpair_f32(a[c], f[4 * c], f[4 * c + 2]);
+          unpair_f32(b[c], f[4 * c + 1], f[4 * c + 3]);
+        }
+      }
+      if (row >= 0 && h < src.n) {
+        store8_bf16(dst + ca, f);
+        store8_bf16(dst + cb, f + 8);
       }
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (HALF) {
-        unpair_f32(a[c], f[2 * c], f[2 * c + 1]);
-        unpair_f32(b[c], f[8 + 2 * c], f[9 + 2 * c]);
-      } else {
-        unpair_f32(a[c], f[4 * c], f[4 * c + 2]);
-        unpair_f32(b[c], f[4 * c + 1], f[4 * c + 3]);
-      }
-    }
-    if (row < 0 || h >= src.n) continue;
-    uint16_t* dst = kind == 0 ? p.out_q + (t * p.q.n + h) * D
-                    : paged   ? (kind == 1 ? p.kpages : p.vpages) + (row * src.n + h) * D
-                              : p.out_k + (t * p.k.n + h) * D;
-    store8_bf16(dst + ca, f);
-    store8_bf16(dst + cb, f + 8);
-  }
+  };
+  if (q0) walk(p.q, q0, p.out_q + t * p.q.n * D, turns, w_s[0], k0);
+  if (k0) walk(p.k, k0, paged ? p.kpages + row * p.k.n * D : p.out_k + t * p.k.n * D, turns, w_s[1], v0);
+  if (v0) walk(p.v, v0, p.vpages + row * p.v.n * D, false, nullptr, nullptr);
 }
 
 }  // namespace pivot
