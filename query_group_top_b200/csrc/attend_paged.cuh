@@ -38,10 +38,6 @@ struct AttendPagedParams {
   int* status;
 };
 
-__device__ __forceinline__ float round_bf16(float x) {
-  return __uint_as_float(pack_bf16(x, 0.f) << 16);
-}
-
 template <int D>
 __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __grid_constant__ AttendPagedParams p) {
   using R = KvRing<D>;

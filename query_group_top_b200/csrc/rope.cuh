@@ -65,6 +65,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float round_bf16(float x) { return __uint_as_float(pack_bf16(x, 0.f) << 16); }
+
 // Eight channels as they lie in memory, and as fp32.
 template <class T>
 struct Vec8;
