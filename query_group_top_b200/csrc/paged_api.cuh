@@ -147,22 +147,26 @@ constexpr int kFewRows = 16;   // packed rows of a sequence up to which attend_r
 AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int sms) {
   AttendPlan a{};
   const long long rows = static_cast<long long>(T) * (Hq / Hk);
-  // At 16 rows a sequence the two take the same (two sequences of 32000, 8 key
-  // heads: 56 us), at 24 the matrix tiles 34 us for 61 (16 sequences of 2000).
-  a.tiles = rows > static_cast<long long>(kFewRows) * B;
-  a.rows = a.tiles ? 256 : rows <= 8ll * B ? 8 : 16;
   a.min_chunk = 256;
-  const long long ctas = B * ((rows + static_cast<long long>(B) * a.rows - 1) / (static_cast<long long>(B) * a.rows)) * Hk;
   const long long most = (max_seqlen + a.min_chunk - 1) / a.min_chunk;
-  const double part_bytes = static_cast<double>(T) * Hq * d * 8;   // a part of every row written and read
+  const double part_time = static_cast<double>(T) * Hq * d * 8 / 5000;   // a part of every row written and read
+  auto units = [&](long long per_cta) { return (rows + B * per_cta - 1) / (B * per_cta) * B * Hk; };
+  // Up to 16 rows a sequence the matrix tiles gain nothing (two sequences of
+  // 32000, 8 key heads: 56 us either way); at 24 they take 34 us for 61 (16
+  // sequences of 2000).  Many short sequences cost either kernel its CTAs (1500
+  // of 120 keys, 20 rows, 8 key heads of 64: 692 us by tiles, 728 by rows).
+  a.tiles = rows > static_cast<long long>(kFewRows) * B;
   if (a.tiles) {
-    // a key tile of both row tiles takes 1.4 us (1.1 at 64 channels), what comes before and after some 6 us
-    a.nsplit = best_parts(ctas, sms, max_seqlen, PartCost{(d == 128 ? 1400. : 1100.) / 128, 6000, 6000, part_bytes / 5000}, most);
+    // 1.4 us a key tile of both row tiles (1.1 at 64 channels), some 6 us before and after
+    a.rows = 256;
+    a.nsplit = best_parts(units(256), sms, max_seqlen,
+                          PartCost{(d == 128 ? 1400. : 1100.) / 128, 6000, 6000, part_time}, most);
   } else {
     // an SM's share of the memory's rate, among its CTAs; some 3 us before and after
+    a.rows = rows <= 8ll * B ? 8 : 16;
     const int per_sm = d == 128 ? KvRing<128>::PER_SM : KvRing<64>::PER_SM;
-    a.nsplit = best_parts(ctas, static_cast<long long>(per_sm) * sms, max_seqlen,
-                          PartCost{4. * d / 41. * per_sm, 3300, 4500, part_bytes / 5000}, most);
+    a.nsplit = best_parts(units(a.rows), static_cast<long long>(per_sm) * sms, max_seqlen,
+                          PartCost{4. * d / 41. * per_sm, 3300, 4500, part_time}, most);
   }
   // the matrix tiles' launch for long chunks among single tokens, which may find
   // none: two parts at most, so that it is over soon

@@ -68,9 +68,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 
 // The row tile `flat` of the batch: which sequence, and which of its tiles of
-// `rows` packed rows.  One warp; without cu every sequence has the same number
-// of tiles, else the tile counts of the sequences that the launch takes are
-// summed 32 at a time.  Returns -1 behind the last tile.
+// `rows` packed rows; -1 where there is none.  One warp.
+//  * Without cu every sequence has the same number of tiles.
+//  * With cu, sequence b's tiles start at floor(cu[b] grp / rows) + b, which
+//    leaves each its own (ceil(n grp / rows) of them fit before the next start)
+//    and needs no sums: b is found by 32 probes a round.  Some places stay empty.
+//  * A launch for the sequences of many rows alone would leave most places empty:
+//    there the tile counts of those are summed, 128 sequences at a time.
 __device__ __forceinline__ int locate_tile(const PagedAttendParams& a, int rows, int flat, int lane, int* tile) {
   const PagedRows& p = a.rows;
   if (!p.cu) {
@@ -78,17 +82,31 @@ __device__ __forceinline__ int locate_tile(const PagedAttendParams& a, int rows,
     *tile = flat % per;
     return flat / per < p.B ? flat / per : -1;
   }
-  int before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    int n = 0;
-    if (b < p.B) {
-      const NewSpan sp = p.span(b);
-      const int packed = sp.n * a.grp;
-      if (packed > a.over && packed <= a.upto) n = static_cast<int>((static_cast<long long>(packed) + rows - 1) / rows);
-      if (!sp.ok) atomicOr(a.status, kStBadLen);
+  if (a.over == 0) {
+    auto start = [&](int b) { return static_cast<long long>(p.cu[b]) * a.grp / rows + b; };
+    int lo = 0, hi = p.B;   // the answer is in [lo, hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const unsigned votes = __ballot_sync(0xffffffffu, at < hi && start(at) <= flat) | 1u;
+      lo += (31 - __clz(votes)) * step;
+      hi = min(hi, lo + step);
     }
-    int sum = n;
+    const long long t = flat - start(lo);
+    if (t < 0 || t > flat || p.new_tokens(lo) * a.grp > a.upto) return -1;
+    *tile = static_cast<int>(t);
+    return lo;
+  }
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 128) {
+    int n[4], sum = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int b = b0 + 4 * lane + x;
+      const int packed = b < p.B ? p.new_tokens(b) * a.grp : 0;
+      n[x] = packed > a.over && packed <= a.upto ? static_cast<int>((static_cast<long long>(packed) + rows - 1) / rows) : 0;
+    }
+    const int mine = n[0] + n[1] + n[2] + n[3];
+    sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -96,9 +114,16 @@ __device__ __forceinline__ int locate_tile(const PagedAttendParams& a, int rows,
     }
     const unsigned past = __ballot_sync(0xffffffffu, before + sum > flat);
     if (past) {
+      // in the first lane whose sum passes: its first sequence that does
       const int l = __ffs(past) - 1;
-      *tile = flat - (before + __shfl_sync(0xffffffffu, sum - n, l));
-      return b0 + l;
+      int left = flat - (before + sum - mine), x = 0;
+      while (x < 3 && left >= n[0]) {
+        left -= n[0];
+        n[0] = n[1], n[1] = n[2], n[2] = n[3];
+        ++x;
+      }
+      *tile = __shfl_sync(0xffffffffu, left, l);
+      return b0 + 4 * l + __shfl_sync(0xffffffffu, x, l);
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
@@ -278,6 +303,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
   const int b = seq_s[0], r0 = seq_s[1] * ROWS;
   if (b < 0) return;
   const NewSpan sp = p.rows.span(b);
+  if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
   const int nrows = min(ROWS, sp.n * p.grp - r0);
   if (nrows <= 0) return;
   const int pos0 = sp.len - sp.n + p.self_key;             // lim of the sequence's first new token
@@ -285,7 +311,6 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
   auto row_of = [&](int r) {
     return (static_cast<long long>(sp.tok0) + (r0 + r) / p.grp) * p.Hq + hk * p.grp + (r0 + r) % p.grp;
   };
-  if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
   const int chunk = chunk_of(sp, p);
   const int kbeg = split * chunk;
   const int kend = min(lim_of(nrows - 1), kbeg + chunk);

@@ -149,8 +149,8 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if (b < 0) return;
   const NewSpan sp = p.rows.span(b);
   const int total = sp.n * p.grp;                           // packed rows of the sequence
-  if (r0 >= total) return;
   if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
+  if (r0 >= total) return;
   const int pos0 = sp.len - sp.n + p.self_key;
   auto lim_of = [&](int r) { return sp.ok ? pos0 + r / p.grp : 0; };
   const int chunk = chunk_of(sp, p);

@@ -50,6 +50,12 @@ struct PagedRows {
     s.ok = in && len >= hi - lo && len <= max_len;
     return s;
   }
+  // The new tokens of sequence b, 0 where its offsets do not fit (span(b).n).
+  PIVOT_HD int new_tokens(int b) const {
+    if (!cu) return g;
+    const long long lo = cu[b], hi = cu[b + 1];
+    return lo >= 0 && hi >= lo && hi <= T ? static_cast<int>(hi - lo) : 0;
+  }
   // Page that holds row r of sequence b (0 <= r < max_len), or -1 where the
   // table names a page outside the cache.
   PIVOT_HD int page(int b, int r) const {

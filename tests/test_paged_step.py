@@ -114,7 +114,8 @@ def rows_lib(tmp_path_factory):
                    'extern "C" void span(const int* t, const int* sl, const int* cu, int B, int T, int g, int mp, int np, '
                    'int lg, int ml, int b, int* out) {\n'
                    '  PagedRows p{t, sl, cu, B, T, g, mp, np, lg, paged_max_len(mp, lg, ml)};\n'
-                   '  NewSpan s = p.span(b); out[0] = s.tok0; out[1] = s.n; out[2] = s.len; out[3] = s.ok;\n}\n'
+                   '  NewSpan s = p.span(b); out[0] = s.tok0; out[1] = s.n; out[2] = s.len; out[3] = s.ok;\n'
+                   '  out[4] = p.new_tokens(b);\n}\n'
                    'extern "C" long long row(const int* t, int mp, int np, int lg, int b, int r) {\n'
                    '  PagedRows p{t, nullptr, nullptr, 1, 1, 1, mp, np, lg, 1 << 30}; return p.row(b, r);\n}\n')
     so = d / "rows.so"
@@ -129,9 +130,10 @@ def test_spans_and_pages_that_do_not_fit_are_refused(rows_lib):
     def span(sl, cu, T, g, mp, lg, ml, b):
         sl = (ctypes.c_int * len(sl))(*sl)
         c = None if cu is None else (ctypes.c_int * len(cu))(*cu)
-        out = (ctypes.c_int * 4)()
+        out = (ctypes.c_int * 5)()
         rows_lib.span(None, sl, c, len(sl), T, g, mp, 9, lg, ml, b, out)
-        return list(out)
+        assert out[4] == out[1]
+        return list(out)[:4]
 
     assert span([5, 7], None, 4, 2, 1, 4, 100, 1) == [2, 2, 7, 1]
     assert span([5, 1], None, 4, 2, 1, 4, 100, 1)[3] == 0                # fewer rows than new ones
@@ -506,6 +508,20 @@ def test_paged_attention_bad_lengths_pages_and_rows_behind():
         good, _ = attend(c, q[:12], True, True)
         assert qg.sync_status() == 0
         assert same_bits(out[:3], good[:3]) and same_bits(out[9:12], good[9:])
+    # offsets that do not fit: told, and the sequences that do fit are right
+    odd = cu.clone()
+    odd[4] = 40
+    out = torch.full((14, H, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    qg.paged_attention(q, c.kpages, c.vpages, c.table, c.seqlens, c.longest, cu_q=odd, out=out)
+    with pytest.raises(qg.PivotError):
+        qg.sync_status()
+    assert same_bits(out[:9], good[:9]) and bool((out[9:] == 9).all())
+    # a length that does not fit, of a sequence without new tokens
+    odd, lens = torch.tensor([0, 3, 3, 6, 9], dtype=torch.int32, device="cuda"), c.seqlens.clone()
+    lens[1], lens[2] = 100000, 53
+    qg.paged_attention(q, c.kpages, c.vpages, c.table, lens, c.longest, cu_q=odd)
+    with pytest.raises(qg.PivotError):
+        qg.sync_status()
     # pages outside the cache are left out and reported
     t = c.table.clone()
     t[0, 0], t[3, 0] = -1, c.kpages.shape[0] + 5
@@ -518,13 +534,14 @@ def test_paged_attention_bad_lengths_pages_and_rows_behind():
 @gpu
 def test_paged_attention_many_sequences_one_long():
     """More sequences than a warp, chunks of one token next to one of many, and no new token in most."""
-    new = [0] * 30 + [200] + [1] * 40 + [0] * 5 + [3]
-    held = [i * 7 % 50 + 1 for i in range(len(new))]
-    c = ref.Cache(held, new, 1, 64, 32, seed=9)
-    q = normal((sum(new), 3, 64), 61)
-    out, lse = attend(c, q, True, True)
-    assert qg.sync_status() == 0
-    check_attention(c, q, out, lse, True, 0.125)
+    for new in ([0] * 30 + [200] + [1] * 40 + [0] * 5 + [3], [1] * 3 + [0] * 126 + [5] + [i % 3 for i in range(200)] + [60],
+                [30] * 2 + [17 + i % 5 for i in range(140)]):
+        held = [i * 7 % 50 + 1 for i in range(len(new))]
+        c = ref.Cache(held, new, 1, 64, 32, seed=9)
+        q = normal((sum(new), 3, 64), 61)
+        out, lse = attend(c, q, True, True)
+        assert qg.sync_status() == 0
+        check_attention(c, q, out, lse, True, 0.125)
 
 
 @gpu
