@@ -142,6 +142,7 @@ struct AttendPlan {
   size_t part_lse, total;   // workspace: the parts' rows at 0, their lse at part_lse
 };
 
+constexpr int kMixedRows = 512;   // packed rows of a batch above which a long chunk in it is looked for
 constexpr int kFewRows = 16;   // packed rows of a sequence up to which attend_rows_kernel takes it
 
 AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int sms) {
@@ -154,7 +155,7 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int 
   // Up to 16 rows a sequence the matrix tiles gain nothing (two sequences of
   // 32000, 8 key heads: 56 us either way); at 24 they take 34 us for 61 (16
   // sequences of 2000).  Many short sequences cost either kernel its CTAs (1500
-  // of 120 keys, 20 rows, 8 key heads of 64: 692 us by tiles, 728 by rows).
+  // of 120 keys, 20 rows, 8 key heads of 64: 571 us by tiles, 728 by rows).
   a.tiles = rows > static_cast<long long>(kFewRows) * B;
   if (a.tiles) {
     // 1.4 us a key tile of both row tiles (1.1 at 64 channels), some 6 us before and after
@@ -228,7 +229,8 @@ int launch_attend(PagedAttendParams ap, const AttendPlan& pl, int most_new, cuda
     // those of many go to the matrix tiles (a chunk of 512 tokens among 200
     // single ones over 4000 keys, 32 heads over 8: 632 us for 822; where there
     // is none, the launch costs some 4 us, which a bound on the tokens spares).
-    if (!pl.tiles && packed > kFewRows && (most_new == 0 || static_cast<long long>(most_new) * ap.grp > kFewRows)) {
+    // Below kMixedRows no chunk is long enough to need it.
+    if (!pl.tiles && packed > kMixedRows && (most_new == 0 || static_cast<long long>(most_new) * ap.grp > kFewRows)) {
       ap.over = ap.many = kFewRows;
       if (int rc = launch_attend_kernel<D>(ap, true, 256, packed / 256 + std::min(B, packed / (kFewRows + 1)), st)) return rc;
       ap.over = 0;

@@ -483,14 +483,15 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const int w = WIDE ? warp : 0;
   const long long row = WIDE ? static_cast<long long>(blockIdx.x) : static_cast<long long>(blockIdx.x) * 4 + warp;
   const long long rows = static_cast<long long>(p.rows.T) * p.Hq;
-  if (row >= rows) return;
-  const int tok = static_cast<int>(row / p.Hq);
+  // every warp waits, those without a row too: what comes behind this kernel in
+  // the stream must not find the parts' kernel still running
+  const int tok = static_cast<int>(min(row, rows - 1) / p.Hq);
   const NewSpan sp = p.rows.span(find_sequence(p.rows, tok, lane));
-  if (tok < sp.tok0 || tok >= sp.tok0 + sp.n) return;
   const int lim = sp.ok ? sp.len - sp.n + p.self_key + (tok - sp.tok0) : 0;
   const int chunk = chunk_of(sp, p);
   const int parts = max(1, (lim + chunk - 1) / chunk);
   grid_wait();
+  if (row >= rows || tok < sp.tok0 || tok >= sp.tok0 + sp.n) return;
   float m = neg_inf();
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_lse[s * rows + row]);
 #pragma unroll

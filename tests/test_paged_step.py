@@ -550,10 +550,10 @@ def test_paged_attention_many_sequences_one_long():
 def test_paged_attention_chunks_among_single_tokens(page, d, held0):
     """A few rows a sequence on average, but some with many: those go to the matrix tiles, the others do not, whatever
     bound on the new tokens is given, and bad lengths among them are told."""
-    new = [1] * 20 + [90] + [1] * 25 + [0, 2, 9, 1] + [1] * 14
+    new = [1] * 20 + [90] + [1] * 25 + [0, 2, 9, 1] + [1] * 84
     held = [(held0 + 37 * i) % (held0 + 50) for i in range(len(new))]
-    c = ref.Cache(held, new, 2, d, page, seed=23)
-    q = normal((sum(new), 4, d), 63)
+    c = ref.Cache(held, new, 1, d, page, seed=23)
+    q = normal((sum(new), 3, d), 63)          # 693 packed rows, 5 a sequence
     out, lse = attend(c, q, True, True)
     assert qg.sync_status() == 0
     check_attention(c, q, out, lse, True, d ** -0.5)
@@ -568,6 +568,7 @@ def test_paged_attention_chunks_among_single_tokens(page, d, held0):
     with pytest.raises(qg.PivotError):
         qg.sync_status()
     assert same_bits(bad[:20], out[:20]) and bool((bad[20:110] == 0).all()) and same_bits(bad[110:135], out[110:135])
+    assert bool((bad[135:137] == 0).all()) and same_bits(bad[137:], out[137:])
 
 
 @gpu
