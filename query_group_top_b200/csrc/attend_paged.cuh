@@ -1,12 +1,15 @@
 // The sparse attention over index rows (attend.cuh) on a paged cache: keys and
 // values behind a block table, the rows of a decode step.
 //
-// Bound by the gathers, 2 * d * 2 bytes an index.  A CTA takes one (query,
-// head); its four warps take the row's indices 16 at a time through the ring of
+// Bytes: the gathers, 2 * d * 2 an index.  A CTA takes one (query, head); its
+// four warps take the row's indices 16 at a time through the ring of
 // paged_attend.cuh, so that what is on its way does not hang on registers or on
-// the arithmetic.  The index of a
-// step is read two steps before its keys and the page one step before, so
-// neither of the two dependent loads is waited for.
+// the arithmetic.  The index of a step is read two steps before its keys and the
+// page one step before, so neither of the two dependent loads is waited for.
+// What bounds it is the warps' own instructions (some 360 a step, three warps a
+// scheduler, DRAM at 50 %): 32 sequences, steps of two, 16 heads of 128, 2048
+// indices take 159 us.  Merging the rows of two members in a CTA, so that common
+// keys are gathered once (0.68 GB for 1.07), was built and took as long.
 //
 // The products run as there, keys in the rows and the query in the columns of
 // m16n8k16 tiles.  The query stands in all eight columns, so every lane has the
@@ -76,11 +79,12 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
     const int t = tbeg + (warp + it * R::NW) * R::KT + (lane & 15);
     return it < mine && t < tend ? __ldg(row + t) : -1;
   };
+  const SequenceRows rows(p.rows, b);
   auto place = [&](int j) -> int {
     if (j < 0) return -1;
-    const long long at = j < len ? p.rows.row(b, j) : -1;
+    const int at = j < len ? rows.row(j) : -1;
     if (at < 0) atomicOr(p.status, kStBadPage);
-    return static_cast<int>(at);
+    return at;
   };
   int next = place(entry(0));
   int next_entry = entry(1);
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
 #pragma unroll
     for (int s = 0; s + 1 < R::ST; ++s) there[s] = there[s + 1];
     there[R::ST - 1] = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
-    if (it < mine && there[R::ST - 1]) kv.issue(it, at);
+    if (it < mine && there[R::ST - 1]) kv.issue(it, at, there[R::ST - 1] == 0xffffu);
     cp_async_commit();
     next = place(e);
   };

@@ -218,29 +218,39 @@ struct KvRing {
   static_assert(PER_SM * (SMEM + 2048) <= 232448, "shared memory of an SM");
 
   uint32_t ring;
-  const uint8_t* kbase;                                 // the head's first key row, at the lane's 16 bytes
-  long long to_v;                                       // bytes from a key row to its value row
-  long long stride;                                     // bytes from a cache row to the next
+  const uint8_t *kbase, *vbase;                         // the head's first key and value row, at the lane's 16 bytes
+  uint32_t stride;                                      // bytes from a cache row to the next
 
   __device__ __forceinline__ void init(uint8_t* smem, const uint16_t* kpages, const uint16_t* vpages, int heads, int head,
                                        int warp, int lane) {
     ring = smem_u32(smem) + warp * BYTES + (lane / (D / 8)) * ROW + (lane % (D / 8)) * 16;
-    kbase = reinterpret_cast<const uint8_t*>(kpages + static_cast<long long>(head) * D + (lane % (D / 8)) * 8);
-    to_v = reinterpret_cast<const uint8_t*>(vpages) - reinterpret_cast<const uint8_t*>(kpages);
-    stride = static_cast<long long>(heads) * D * 2;
+    const long long at = static_cast<long long>(head) * D + (lane % (D / 8)) * 8;
+    kbase = reinterpret_cast<const uint8_t*>(kpages + at);
+    vbase = reinterpret_cast<const uint8_t*>(vpages + at);
+    stride = static_cast<uint32_t>(heads) * D * 2;
   }
   // Brings in step `it`: lane l and l + 16 have the cache row of key l, -1
   // where there is none (zeros then: 0 * what the ring held may be NaN).
-  __device__ __forceinline__ void issue(int it, int row) {
+  // `whole`, the same in every lane: all 16 are there.
+  __device__ __forceinline__ void issue(int it, int row, bool whole) {
     const uint32_t dst = ring + (it % ST) * (2 * HALF);
     constexpr int RP = 256 / D;                         // rows that a warp's 32 pieces make
+    const int mine = (threadIdx.x & 31) / (D / 8);
+    if (whole) {
 #pragma unroll
-    for (int x = 0; x < KT / RP; ++x) {
-      const int kr = __shfl_sync(0xffffffffu, row, x * RP + (threadIdx.x & 31) / (D / 8));
-      const uint8_t* src = kbase + max(kr, 0) * stride;
-      const uint32_t bytes = kr < 0 ? 0u : 16u;
-      cp_async_16(dst + x * RP * ROW, src, bytes);
-      cp_async_16(dst + x * RP * ROW + HALF, src + to_v, bytes);
+      for (int x = 0; x < KT / RP; ++x) {
+        const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, row, x * RP + mine))) * stride;
+        cp_async_16(dst + x * RP * ROW, kbase + off);
+        cp_async_16(dst + x * RP * ROW + HALF, vbase + off);
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < KT / RP; ++x) {
+        const int kr = __shfl_sync(0xffffffffu, row, x * RP + mine);
+        const uint64_t off = kr < 0 ? 0 : static_cast<uint64_t>(static_cast<uint32_t>(kr)) * stride;
+        cp_async_16(dst + x * RP * ROW, kbase + off, kr < 0 ? 0u : 16u);
+        cp_async_16(dst + x * RP * ROW + HALF, vbase + off, kr < 0 ? 0u : 16u);
+      }
     }
   }
   __device__ __forceinline__ uint32_t keys(int it, uint8_t* smem, int warp) const {
@@ -320,19 +330,20 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
   const int mine = ntiles > warp ? (ntiles - warp + R::NW - 1) / R::NW : 0;
   R kv;
   kv.init(smem, p.kpages, p.vpages, p.Hk, hk, warp, lane);
+  const SequenceRows rows(p.rows, b);
   // cache row of the key that lanes l and l + 16 address in step `it`
   auto place = [&](int it) -> int {
     const int j = kbeg + (warp + it * R::NW) * R::KT + (lane & 15);
     if (it >= mine || j >= kend) return -1;
-    const long long row = p.rows.row(b, j);
+    const int row = rows.row(j);
     if (row < 0) atomicOr(p.status, kStBadPage);
-    return static_cast<int>(row);
+    return row;
   };
   int next = place(0);
   auto issue = [&](int it) {
     const int row = next;
     next = place(it + 1);
-    if (it < mine) kv.issue(it, row);
+    if (it < mine) kv.issue(it, row, __all_sync(0xffffffffu, row >= 0));
     cp_async_commit();
   };
 #pragma unroll

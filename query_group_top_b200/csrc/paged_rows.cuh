@@ -69,6 +69,20 @@ struct PagedRows {
   }
 };
 
+// One sequence's rows: PagedRows::row with the sequence's place in the table
+// taken out, in 32 bits (a cache has fewer than 2^31 rows).
+struct SequenceRows {
+  const int32_t* table;
+  int num_pages, log2_page;
+
+  PIVOT_HD SequenceRows(const PagedRows& p, int b)
+      : table(p.table + static_cast<long long>(b) * p.max_pages), num_pages(p.num_pages), log2_page(p.log2_page) {}
+  PIVOT_HD int row(int r) const {
+    const int pg = table[r >> log2_page];
+    return pg >= 0 && pg < num_pages ? (pg << log2_page) + (r & ((1 << log2_page) - 1)) : -1;
+  }
+};
+
 // Rows [0, max_len) that sequences of a cache may use: no more than the table
 // covers, in an int.
 PIVOT_HD int paged_max_len(int max_pages, int log2_page, int max_seqlen) {

@@ -346,6 +346,9 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
 }
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Shared-memory atomics on a 32-bit shared-window address.  The compiler
 // cannot prove that pointers into the realigned dynamic shared memory are
 // shared, and the generic-address atomics it then emits are several times

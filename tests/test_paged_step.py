@@ -117,7 +117,9 @@ def rows_lib(tmp_path_factory):
                    '  NewSpan s = p.span(b); out[0] = s.tok0; out[1] = s.n; out[2] = s.len; out[3] = s.ok;\n'
                    '  out[4] = p.new_tokens(b);\n}\n'
                    'extern "C" long long row(const int* t, int mp, int np, int lg, int b, int r) {\n'
-                   '  PagedRows p{t, nullptr, nullptr, 1, 1, 1, mp, np, lg, 1 << 30}; return p.row(b, r);\n}\n')
+                   '  PagedRows p{t, nullptr, nullptr, 1, 1, 1, mp, np, lg, 1 << 30}; return p.row(b, r);\n}\n'
+                   'extern "C" int seq_row(const int* t, int mp, int np, int lg, int b, int r) {\n'
+                   '  PagedRows p{t, nullptr, nullptr, 1, 1, 1, mp, np, lg, 1 << 30}; return SequenceRows(p, b).row(r);\n}\n')
     so = d / "rows.so"
     subprocess.check_call(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-I",
                            os.path.join(ROOT, "query_group_top_b200", "csrc"), "-o", str(so), str(src)])
@@ -153,6 +155,9 @@ def test_spans_and_pages_that_do_not_fit_are_refused(rows_lib):
     assert rows_lib.row(table, 3, 9, 4, 0, 32) == -1                     # page -1
     assert rows_lib.row(table, 3, 9, 4, 1, 0) == -1 and rows_lib.row(table, 3, 9, 4, 1, 16) == -1   # pages past the cache
     assert rows_lib.row(table, 3, 9, 4, 1, 47) == 15
+    for b in range(2):
+        for r in range(48):
+            assert rows_lib.seq_row(table, 3, 9, 4, b, r) == rows_lib.row(table, 3, 9, 4, b, r)
     # a cache row behind 32 bits
     far = (ctypes.c_int * 1)(2000000000)
     assert rows_lib.row(far, 1, 2147483647, 8, 0, 255) == 2000000000 * 256 + 255
@@ -675,6 +680,60 @@ def test_sparse_attention_paged_equals_packed(d, page):
     with pytest.raises(qg.PivotError):
         qg.sync_status()
     assert bool((out[2] == 0).all()) and same_bits(out[:2], got[:2])
+
+
+def check_index_rows(c, q, idx, out, what):
+    """Against the definition in 64 bits, every entry as it stands: twice where it stands twice."""
+    d = q.shape[-1]
+    for b in range(q.shape[0]):
+        for i in range(q.shape[1]):
+            for h in range(q.shape[2]):
+                j = idx[b, i, h][idx[b, i, h] >= 0].long()
+                if j.numel() == 0:
+                    assert bool((out[b, i, h] == 0).all())
+                    continue
+                x = c.k[b][j, h].double() @ q[b, i, h].double() * d ** -0.5
+                y = torch.softmax(x, 0) @ c.v[b][j, h].double()
+                # scores of a few units by fp32 sums of d products, weights and sums in fp32: below 2e-5 of values of a
+                # few units
+                far = float((out[b, i, h].double() - y).abs().max())
+                assert far <= 2e-5, f"{what}: sequence {b}, member {i}, head {h}: {far}"
+
+
+@gpu
+@pytest.mark.parametrize("g", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sparse_attention_paged_rows_of_every_kind(d, g):
+    """Members that share all, some or none of their rows; rows of very different lengths; rows that are not ascending,
+    hold an index twice or padding between; few rows (a cluster each) and many."""
+    rng = np.random.default_rng(10 * g + d)
+    for B, H, top_k, held in ((2, 2, 700, [900, 64]), (3, 1, 65, [70, 300, 1]), (40, 4, 64, [100 + i for i in range(40)])):
+        c = ref.Cache(held, [g] * B, H, d, 16, seed=g)
+        q = normal((B, g, H, d), 72)
+        idx = -np.ones((B, g, H, top_k), np.int32)
+        for b in range(B):
+            for h in range(H):
+                pool = rng.permutation(held[b])
+                kind = rng.integers(0, 6)
+                for i in range(g):
+                    n = int(rng.integers(0, min(top_k, held[b]) + 1)) if rng.random() < 0.5 else min(top_k, held[b])
+                    row = np.sort(pool[:n]) if kind == 0 else np.sort(rng.choice(held[b], n, replace=False))
+                    if kind == 1 and i % 2:
+                        row = row[:3]
+                    if kind == 2 and i == 0:
+                        row = rng.permutation(row)
+                    if kind == 3 and len(row) > 4:
+                        row[2] = row[3]
+                    if kind == 4 and len(row) > 4:
+                        row[1] = -1
+                    if kind == 5 and i % 2:
+                        row = row + 0 if i % 4 == 1 else row[:0]
+                    idx[b, i, h, :len(row)] = row
+        idx = torch.from_numpy(idx).cuda()
+        out = qg.sparse_attention_paged(q, c.kpages, c.vpages, c.table, c.seqlens, idx)
+        assert qg.sync_status() == 0
+        check_index_rows(c, q, idx, out, f"B={B}")
+        assert same_bits(out, qg.sparse_attention_paged(q, c.kpages, c.vpages, c.table, c.seqlens, idx))
 
 
 # ------------------------------------------------------------------ together
