@@ -6,10 +6,11 @@
 // paged_attend.cuh, so that what is on its way does not hang on registers or on
 // the arithmetic.  The index of a step is read two steps before its keys and the
 // page one step before, so neither of the two dependent loads is waited for.
-// What bounds it is the warps' own instructions (some 360 a step, three warps a
-// scheduler, DRAM at 50 %): 32 sequences, steps of two, 16 heads of 128, 2048
-// indices take 159 us.  Merging the rows of two members in a CTA, so that common
-// keys are gathered once (0.68 GB for 1.07), was built and took as long.
+// What bounds it is the chain of a step in its warp (rows, product, softmax,
+// product), three warps a scheduler: DRAM is at 50 %, the issue slots at 29.  32
+// sequences, steps of two, 16 heads of 128, 2048 indices take 155 us.  Merging the
+// rows of two members in a CTA, so that common keys are gathered once (0.68 GB for
+// 1.07), was built and took 173 to 182.
 //
 // The products run as there, keys in the rows and the query in the columns of
 // m16n8k16 tiles.  The query stands in all eight columns, so every lane has the
