@@ -467,6 +467,8 @@ def _like(out, x, dtype, name):
 
 def _pages(kpages, vpages, dev, d):
     """(num_pages, page_size, heads) of a paged cache."""
+    if not isinstance(kpages, torch.Tensor):
+        raise PivotError("kpages must be a tensor")
     sh = kpages.shape
     if (kpages.dtype is not torch.bfloat16 or len(sh) != 4 or sh[3] != d or kpages.get_device() != dev
             or not kpages.is_contiguous()):
@@ -643,6 +645,10 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
         raise PivotError(f"q's heads must be a multiple of the cache's {Hk} (got {Hq})")
     T, B, g, max_pages, pcu, psl, pbt = _sequences(sh, cu_q, seqlens, block_table, dev, "cu_q")
     max_seqlen = int(max_seqlen)
+    if not 1 <= max_seqlen < 1 << 30:
+        raise PivotError(f"max_seqlen must be in [1, 2^30) (got {max_seqlen})")
+    if vpages is None:
+        raise PivotError("paged_attention needs vpages")
     if max_q is not None and cu_q is not None:
         if max_q < 1:
             raise PivotError("max_q must be >= 1")
@@ -682,6 +688,8 @@ def sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out=Non
     T, B, g, max_pages, _, psl, pbt = _sequences(sh, None, seqlens, block_table, dev, "cu_q")
     if not isinstance(idx, torch.Tensor) or idx.dim() != 4:
         raise PivotError("idx must be an int32 tensor [B, g, H, top_k]")
+    if vpages is None:
+        raise PivotError("sparse_attention_paged needs vpages")
     top_k = idx.shape[3]
     pidx = _int32("idx", idx, dev, (B, g, H, top_k))
     with _On(dev, stream, (q, kpages, vpages, block_table, seqlens, idx, out)) as raw:

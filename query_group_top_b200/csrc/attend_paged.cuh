@@ -199,7 +199,23 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
     }
     cluster.sync();   // no CTA leaves while its part is being read
   }
-  if (c < D && rank == 0) p.out[static_cast<long long>(rh) * D + c] = cl == 0.f ? 0.f : acc / cl;
+  if (rank > 0) return;
+  const float value = cl == 0.f ? 0.f : acc / cl;          // 0 in threads without a channel
+  // an infinite value under a weight whose lower terms are zero came in as 0 * inf
+  if (!__syncthreads_or(!(fabsf(value) < __int_as_float(0x7f800000)))) {
+    if (c < D) p.out[static_cast<long long>(rh) * D + c] = value;
+  } else if (warp == 0) {
+    float e[D / 32], lse2;
+    attend_row_exact<D>(
+        p, p.H, h, rh, 0, p.top_k,
+        [&](int t) {
+          const int j = __ldg(row + t);
+          return j >= 0 && j < len ? rows.row(j) : -1;
+        },
+        lane, e, &lse2);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) p.out[static_cast<long long>(rh) * D + lane * (D / 32) + x] = e[x];
+  }
 }
 
 }  // namespace pivot

@@ -130,13 +130,14 @@ __device__ __forceinline__ int locate_tile(const PagedAttendParams& a, int rows,
   return -1;
 }
 
-// One row over the keys [j0, j1) by a whole warp, key after key, reading only
-// those keys: lane l holds channels [l * D/32, ...).  For rows whose tile gave
-// a value that is not finite: there a masked position's infinity or NaN may
-// have come in as 0 * inf, and here it does not.
-template <int D>
-__device__ __forceinline__ void attend_row_exact(const PagedAttendParams& p, int b, int hk, long long qrow, int j0,
-                                              int j1, int lane, float (&o)[D / 32], float* lse2) {
+// One query row over the keys j0 <= j < j1, key j in cache row row_of(j) (-1:
+// left out, -2: zeros), by a whole warp, key after key, reading only those keys: lane l holds
+// channels [l * D/32, ...).  For rows whose tile gave a value that is not
+// finite: there a masked position's infinity or NaN, or a weight's part that
+// rounds to zero, may have come in as 0 * inf, and here it does not.
+template <int D, class P, class RowOf>
+__device__ __forceinline__ void attend_row_exact(const P& p, int heads, int head, long long qrow, int j0, int j1,
+                                              RowOf row_of, int lane, float (&o)[D / 32], float* lse2) {
   constexpr int C = D / 32;
   float q[C], m = neg_inf(), l = 0.f;
 #pragma unroll
@@ -145,12 +146,12 @@ __device__ __forceinline__ void attend_row_exact(const PagedAttendParams& p, int
     o[c] = 0.f;
   }
   for (int j = j0; j < j1; ++j) {
-    const long long row = p.rows.row(b, j);
-    if (row < 0) continue;
-    const long long at = (row * p.Hk + hk) * D + lane * C;
+    const long long row = row_of(j);
+    if (row == -1) continue;
+    const long long at = (row * heads + head) * D + lane * C;
     float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) s = fmaf(q[c], __uint_as_float(static_cast<uint32_t>(p.kpages[at + c]) << 16), s);
+    for (int c = 0; c < C; ++c) s = fmaf(q[c], row < 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(p.kpages[at + c]) << 16), s);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
     s *= p.scale_log2;
@@ -160,8 +161,9 @@ __device__ __forceinline__ void attend_row_exact(const PagedAttendParams& p, int
     l = l * f + e;
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      o[c] = fmaf(e, __uint_as_float(static_cast<uint32_t>(p.vpages[at + c]) << 16), o[c] * f);
+      o[c] = fmaf(e, row < 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(p.vpages[at + c]) << 16), o[c] * f);
     m = mn;
+    if (e != e) break;   // all is NaN from here on, whatever follows
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -465,7 +467,8 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
     }
     const long long row = row_of(r);
     if (!__all_sync(0xffffffffu, fine))
-      attend_row_exact<D>(p, b, hk, row, kbeg, min(kend, lim_of(r)), lane, acc, &lse2);
+      attend_row_exact<D>(p, p.Hk, hk, row, kbeg, min(kend, lim_of(r)), [&](int j) { return rows.row_or(j, -2); }, lane,
+                          acc, &lse2);
     if (p.part_o) {
       const long long at = static_cast<long long>(split) * p.rows.T * p.Hq + row;
 #pragma unroll

@@ -587,12 +587,14 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           p.lse[row] = lse2 * kLn2;
       }
       // rows with a value that is not finite, one by one over the keys that they see alone
+      __syncwarp();   // (their first result, written by the row's own lane, comes before)
       for (unsigned todo = __ballot_sync(0xffffffffu, row_ok && !fine); todo; todo &= todo - 1) {
         const int x = __ffs(todo) - 1;
         const long long rx = __shfl_sync(0xffffffffu, row, x);
         const int lx = __shfl_sync(0xffffffffu, lim, x);
         float o[D / 32], z;
-        attend_row_exact<D>(p, b, hk, rx, kbeg, min(lx, kbeg + chunk), lane, o, &z);
+        attend_row_exact<D>(p, p.Hk, hk, rx, kbeg, min(lx, kbeg + chunk),
+                            [&](int j) { return SequenceRows(p.rows, b).row_or(j, -2); }, lane, o, &z);
         if (p.part_o) {
           const long long ax = static_cast<long long>(split) * p.rows.T * p.Hq + rx;
 #pragma unroll

@@ -77,9 +77,10 @@ struct SequenceRows {
 
   PIVOT_HD SequenceRows(const PagedRows& p, int b)
       : table(p.table + static_cast<long long>(b) * p.max_pages), num_pages(p.num_pages), log2_page(p.log2_page) {}
-  PIVOT_HD int row(int r) const {
+  PIVOT_HD int row(int r) const { return row_or(r, -1); }
+  PIVOT_HD int row_or(int r, int none) const {
     const int pg = table[r >> log2_page];
-    return pg >= 0 && pg < num_pages ? (pg << log2_page) + (r & ((1 << log2_page) - 1)) : -1;
+    return pg >= 0 && pg < num_pages ? (pg << log2_page) + (r & ((1 << log2_page) - 1)) : none;
   }
 };
 

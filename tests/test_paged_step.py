@@ -736,6 +736,72 @@ def test_sparse_attention_paged_rows_of_every_kind(d, g):
         assert same_bits(out, qg.sparse_attention_paged(q, c.kpages, c.vpages, c.table, c.seqlens, idx))
 
 
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,top_k", [(1, 40), (60, 90)])
+def test_sparse_attention_paged_takes_infinite_values_as_they_are(d, B, top_k):
+    """A selected value that is infinite or NaN comes out as the definition has it, channel by channel (a cluster a
+    row, and one CTA); a key that is NaN makes its queries NaN; rows that select neither are untouched."""
+    H = 12
+    c = ref.Cache([120] * B, [1] * B, H, d, 16, seed=21)
+    q = normal((B, 1, H, d), 91)
+    idx = torch.arange(top_k, dtype=torch.int32, device="cuda").expand(B, 1, H, top_k).contiguous()
+    idx[:, :, 1] += 9                                # leaves out rows 0 to 8
+    clean = qg.sparse_attention_paged(q, c.kpages, c.vpages, c.table, c.seqlens, idx)
+    pg = int(c.table[0, 0])
+    c.vpages[pg, 5, 0, 3:6] = torch.tensor([math.inf, -math.inf, math.nan], device="cuda")
+    c.vpages[pg, 5, 1, :] = math.nan                 # not selected
+    c.kpages[pg, 7, 2, 0] = math.nan
+    out = qg.sparse_attention_paged(q, c.kpages, c.vpages, c.table, c.seqlens, idx)
+    assert qg.sync_status() == 0
+    want = clean.clone()
+    want[0, 0, 0, 3:6] = torch.tensor([math.inf, -math.inf, math.nan], device="cuda")
+    want[0, 0, 2] = math.nan
+    whole = torch.isfinite(want)
+    assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out[torch.isinf(want)], want[torch.isinf(want)])
+    ref.close(out[whole], want[whole].double(), torch.full_like(want[whole].double(), 2e-5), "the finite ones")
+
+
+@gpu
+@pytest.mark.parametrize("new", [1, 40])
+def test_paged_attention_infinite_values_beside_a_page_that_is_not_there(new):
+    """A page outside the cache reads as zeros also in a row that is worked out key by key."""
+    H, d, page, held = 2, 64, 16, 70
+    c = ref.Cache([held], [new], H, d, page, seed=22)
+    q = normal((new, H, d), 92)
+    t = c.table.clone()
+    t[0, 1] = -1
+    pg = int(c.table[0, 0])
+    c.vpages[pg, 3, 0, 7] = math.inf
+    out = qg.paged_attention(q, c.kpages, c.vpages, t, c.seqlens, c.longest, cu_q=c.cu)
+    with pytest.raises(qg.PivotError):
+        qg.sync_status()
+    k, v = c.k[0].clone(), c.v[0].clone()
+    k[page:2 * page] = 0
+    v[page:2 * page] = 0
+    lim = torch.arange(held + 1, held + new + 1)
+    want, _, bound, _ = ref.attention(q, k, v, lim, d ** -0.5)
+    assert bool((out[:, 0, 7] == math.inf).all())
+    out[:, 0, 7], want[:, 0, 7] = 0, 0
+    ref.close(out, want, bound, "the other channels")
+
+
+@gpu
+def test_attention_without_values_or_with_lengths_past_its_range_is_refused():
+    c = ref.Cache([30, 5], [2, 2], 2, 64, 16, seed=1)
+    q = normal((2, 2, 2, 64), 1)
+    idx = torch.zeros((2, 2, 2, 3), dtype=torch.int32, device="cuda")
+    for m in (1 << 30, (1 << 32) + 64, -1):
+        with pytest.raises(qg.PivotError):
+            qg.paged_attention(q, c.kpages, c.vpages, c.table, c.seqlens, m)
+    with pytest.raises(qg.PivotError):
+        qg.paged_attention(q, c.kpages, None, c.table, c.seqlens, c.longest)
+    with pytest.raises(qg.PivotError):
+        qg.sparse_attention_paged(q, c.kpages, None, c.table, c.seqlens, idx)
+    with pytest.raises(qg.PivotError):
+        qg.paged_attention(q, None, None, c.table, c.seqlens, c.longest)
+
+
 # ------------------------------------------------------------------ together
 def step(c, qkv, Hq, H, d, g, freqs, top_k, Kc):
     """One decode step as a serving loop makes it: append, index, attend over the rows and densely."""
