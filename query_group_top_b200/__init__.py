@@ -22,9 +22,9 @@ The serving step around the indexer, over a paged cache:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
-import struct
 
 import torch
 
@@ -57,13 +57,6 @@ EXPORTED = (
 
 class PivotError(RuntimeError):
     pass
-
-
-# The C ABI's option structs, packed: pivot_heads_t (data, weight, token_stride, head_stride, heads), pivot_rope_t
-# (freqs, amplitude, eps, rot_dim, layout), pivot_attend_t (scale, include_self).
-_HEADS = struct.Struct("@PPqqi4x").pack
-_ROPE = struct.Struct("@Pddii").pack
-_ATTEND = struct.Struct("@di4x").pack
 
 
 def library_path() -> str:
@@ -338,168 +331,35 @@ def sparse_attention(q, k, v, idx, cu_seqlens=None, g=1, out=None, stream=None):
 
 
 # ------------------------------------------------------------------ the serving step over a paged cache
-# These calls are short (a decode step's take a few microseconds on the device), so their checks read each
-# attribute of a tensor once and build what the C call takes from it.
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_LAYOUTS = {"half": 0, "interleaved": 1}
+_calls = None
 
 
-def _raw_stream(index):
-    return torch.cuda.current_stream(index).cuda_stream
+def _load_step():
+    """The compiled half of these calls' binding (csrc/binding.cpp): their checks, outputs, workspaces and the C call."""
+    global _calls
+    lib = load_library()
+    try:
+        m = importlib.import_module(__name__ + "._step")
+    except ImportError as e:
+        raise PivotError(f"the binding of the serving step does not load ({e}): build it with "
+                         "`python -m query_group_top_b200.build`") from e
+    m.bind(PivotError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        "pivot_last_error", "pivot_qk_rope", "pivot_paged_append", "pivot_paged_attention_workspace_size",
+        "pivot_paged_attention", "pivot_sparse_attention_paged")))
+    _calls = m
+    return m
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)     # the same, without a Stream object
-
-
-class _On:
-    """Where a call runs: on the given stream, or on the current one of its tensors' device, with that device made
-    current.  What the call allocates belongs to that stream; inputs that were made on another one are marked as used
-    by it, so that freeing them does not hand their memory out under the call."""
-    __slots__ = ("raw", "ctx")
-
-    def __init__(self, index, stream, tensors):
-        if stream is None:
-            self.raw = _raw_stream(index)
-            self.ctx = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-            return
-        if stream.device.index != index:
-            raise PivotError(f"the stream is of {stream.device}, the tensors are on cuda:{index}")
-        self.raw = stream.cuda_stream
-        if self.raw != _raw_stream(index):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        self.ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
-
-    def __exit__(self, *why):
-        if self.ctx is not None:
-            self.ctx.__exit__(*why)
-
-
-def _tokens(name, x):
-    """(shape, device index) of new tokens' rows x: [T, heads, d], or [B, g, heads, d]."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise PivotError(f"{name} must be a CUDA tensor")
-    sh = x.shape
-    n = len(sh)
-    if n != 3 and n != 4:
-        raise PivotError(f"{name} must be [T, heads, d] or [B, g, heads, d]")
-    d = sh[-1]
-    if d != 64 and d != 128:
-        raise PivotError(f"head_dim must be 64 or 128 (got {d})")
-    return sh, x.get_device()
-
-
-def _heads(name, x, weight, like, dtype, dev):
-    """pivot_heads_t of x: rows of the tokens and channels of shape `like`, of any number of heads; x may be a strided
-    view (a slice of a fused projection)."""
-    sh = x.shape
-    d = like[-1]
-    if len(sh) != len(like) or sh[0] != like[0] or sh[-1] != d or (len(sh) == 4 and sh[1] != like[1]):
-        raise PivotError(f"{name} must be {[*like[:-2]]} tokens of heads of {d} channels (got {[*sh]})")
-    if x.dtype is not dtype or x.get_device() != dev:
-        raise PivotError(f"{name} must be {dtype} on cuda:{dev}, as the call's other tensors (is {x.dtype} on {x.device})")
-    H, ptr = sh[-2], x.data_ptr()
-    if x.is_contiguous():
-        ts, hs = H * d, d
-    else:
-        st = x.stride()
-        if st[-1] != 1:
-            raise PivotError(f"{name}'s channels must be adjacent")
-        ts = st[-3]
-        if len(sh) == 4:
-            if sh[1] == 1:
-                ts = st[0]
-            elif sh[0] > 1 and st[0] != sh[1] * ts:
-                raise PivotError(f"{name}'s tokens must be evenly spaced (strides {st})")
-        if x.numel() == d * H:
-            ts = 0
-        hs = st[-2] if H > 1 else 0
-        step = 16 // x.element_size()
-        if ts % step or hs % step:
-            raise PivotError(f"{name}'s rows must start on 16-byte boundaries")
-    if ptr % 16 or H < 1:
-        raise PivotError(f"{name}'s rows must start on 16-byte boundaries")
-    if weight is None:
-        return _HEADS(ptr, 0, ts, hs, H)
-    w = weight.data_ptr()
-    if weight.dtype is not dtype or weight.shape != (d,) or weight.get_device() != dev or w % 16 or not weight.is_contiguous():
-        raise PivotError(f"{name}_weight must be a contiguous, 16-byte aligned {dtype} tensor of {d} channels on cuda:{dev}")
-    return _HEADS(ptr, w, ts, hs, H)
-
-
-def _rope(freqs, layout, amplitude, eps, d, dev):
-    lay = _LAYOUTS.get(layout)
-    if lay is None:
-        raise PivotError('layout must be "half" or "interleaved"')
-    if not (0.0 <= eps < math.inf and -math.inf < amplitude < math.inf):
-        raise PivotError("eps must be >= 0, and eps and amplitude finite")
-    if freqs is None:
-        return _ROPE(0, 1.0, eps, 0, 0)
-    if freqs.dtype is not torch.float64 or freqs.dim() != 1 or freqs.get_device() != dev or not freqs.is_contiguous():
-        raise PivotError(f"freqs must be a contiguous float64 vector of rot_dim / 2 frequencies on cuda:{dev}")
-    rot = 2 * freqs.numel()
-    if rot < 16 or rot > d or rot % 16:
-        raise PivotError(f"rot_dim must be a multiple of 16 in [16, d] (got {rot})")
-    return _ROPE(freqs.data_ptr(), amplitude, eps, rot, lay)
-
-
-def _int32(name, t, dev, shape):
-    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev
-            or not t.is_contiguous()):
-        raise PivotError(f"{name} must be a contiguous int32 tensor of shape {[*shape]} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _like(out, x, dtype, name):
-    """`out` checked, or a new contiguous tensor of x's shape."""
-    if out is not None:
-        return _out(out, x.shape, dtype, x.device, name)
-    if x.is_contiguous():    # (empty_like takes a third of empty's host time, and keeps the strides)
-        return torch.empty_like(x) if x.dtype is dtype else torch.empty_like(x, dtype=dtype)
-    return torch.empty(x.shape, dtype=dtype, device=x.device)
-
-
-def _pages(kpages, vpages, dev, d):
-    """(num_pages, page_size, heads) of a paged cache."""
-    if not isinstance(kpages, torch.Tensor):
-        raise PivotError("kpages must be a tensor")
-    sh = kpages.shape
-    if (kpages.dtype is not torch.bfloat16 or len(sh) != 4 or sh[3] != d or kpages.get_device() != dev
-            or not kpages.is_contiguous()):
-        raise PivotError(f"kpages must be contiguous bfloat16 [num_pages, page_size, heads, {d}] on cuda:{dev}")
-    if vpages is not None and (vpages.dtype is not torch.bfloat16 or vpages.shape != sh or vpages.get_device() != dev
-                               or not vpages.is_contiguous()):
-        raise PivotError(f"vpages must be contiguous bfloat16 {[*sh]} on cuda:{dev}, as kpages")
-    n, page, H, _ = sh
-    if page & (page - 1) or page < 1:
-        raise PivotError(f"page_size must be a power of two (got {page})")
-    if n < 1 or H < 1:
-        raise PivotError("the cache has no pages or no heads")
-    return n, page, H
-
-
-def _sequences(sh, cu, seqlens, block_table, dev, cu_name):
-    """(T, B, g, max_pages, pointer of cu, of seqlens, of block_table) of a call's new tokens of shape sh."""
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 or block_table.shape[1] < 1:
-        raise PivotError("block_table must be an int32 tensor [B, max_pages]")
-    bt = block_table.shape
-    B = bt[0]
-    if cu is None:
-        if len(sh) != 4 or sh[0] != B:
-            raise PivotError(f"without {cu_name}, the new tokens are [B, g, heads, d] with block_table's B = {B}")
-        g, pcu = sh[1], None
-        T = B * g
-    else:
-        if len(sh) != 3:
-            raise PivotError(f"with {cu_name}, the new tokens are [T, heads, d]")
-        g, T, pcu = 0, sh[0], _int32(cu_name, cu, dev, (B + 1,))
-    return T, B, g, bt[1], pcu, _int32("seqlens", seqlens, dev, (B,)), _int32("block_table", block_table, dev, bt)
+def _on(stream, *tensors):
+    """The context of a call on a given stream: what the call allocates belongs to it, and inputs that were made on
+    another one are marked as used by it, so that freeing them does not hand their memory out under the call."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            if t.device != stream.device:
+                raise PivotError(f"the stream is of {stream.device}, a tensor is on {t.device}")
+            if stream != torch.cuda.current_stream(t.device):
+                t.record_stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=None, beta_fast=32.0,
@@ -548,38 +408,11 @@ def qk_rope(q, k, positions, freqs, layout="half", amplitude=1.0, q_weight=None,
     positions: int32, one a token; freqs: float64 [rot_dim / 2] (rope_frequencies; None: norm only); layout: pairs
     (i, i + rot_dim / 2) ("half") or (2 i, 2 i + 1) ("interleaved"); the channels behind rot_dim stay.  fp32
     arithmetic, angles reduced in fp64.  Returns (q, k) in bf16, contiguous; out_q, out_k may be the bf16 inputs."""
-    lib = _lib or load_library()
-    x = q if q is not None else k
-    if x is None:
-        raise PivotError("qk_rope needs q or k")
-    sh, dev = _tokens("q" if q is not None else "k", x)
-    dtype = x.dtype
-    if dtype not in _DTYPES:
-        raise PivotError(f"q and k must be bfloat16, float16 or float32 (got {dtype})")
-    if (q is None and q_weight is not None) or (k is None and k_weight is not None):
-        raise PivotError("a norm weight without its heads")
-    hq = None if q is None else _heads("q", q, q_weight, sh, dtype, dev)
-    hk = None if k is None else _heads("k", k, k_weight, sh, dtype, dev)
-    rope = _rope(freqs, layout, amplitude, eps, sh[-1], dev)
-    T = sh[0] if len(sh) == 3 else sh[0] * sh[1]
-    pos = None
-    if freqs is not None:
-        if positions is None or positions.numel() != T:
-            raise PivotError("positions must hold one int32 position a token")
-        pos = _int32("positions", positions, dev, positions.shape)
-    with _On(dev, stream, (q, k, positions, freqs, q_weight, k_weight, out_q, out_k)) as raw:
-        pq = pk = None
-        if q is not None:
-            out_q = _like(out_q, q, torch.bfloat16, "out_q")
-            pq = out_q.data_ptr()
-        if k is not None:
-            out_k = _like(out_k, k, torch.bfloat16, "out_k")
-            pk = out_k.data_ptr()
-        if T:
-            rc = lib.pivot_qk_rope(hq, hk, _DTYPES[dtype], pos, rope, T, sh[-1], pq, pk, raw)
-            if rc:
-                _err(lib, rc)
-    return out_q if q is not None else None, out_k if k is not None else None
+    step = _calls or _load_step()
+    if stream is None:
+        return step.qk_rope(q, k, positions, freqs, layout, amplitude, q_weight, k_weight, eps, out_q, out_k)
+    with _on(stream, q, k, positions, freqs, q_weight, k_weight, out_q, out_k):
+        return step.qk_rope(q, k, positions, freqs, layout, amplitude, q_weight, k_weight, eps, out_q, out_k)
 
 
 def paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new=None, freqs=None, layout="half", amplitude=1.0,
@@ -594,34 +427,13 @@ def paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new=None, freqs=
     indexer and the attention then take: token i of n_b goes to row seqlens[b] - n_b + i.  Returns the queries in
     bf16 (None without q).  Sequences that do not fit their table and pages outside the cache are left out and
     reported by sync_status()."""
-    lib = _lib or load_library()
-    sh, dev = _tokens("k", k)
-    d, Hk, dtype = sh[-1], sh[-2], k.dtype
-    if dtype not in _DTYPES:
-        raise PivotError(f"k, v and q must be bfloat16, float16 or float32 (got {dtype})")
-    if (v is None) != (vpages is None):
-        raise PivotError("v and vpages go together")
-    if q is None and (out_q is not None or q_weight is not None):
-        raise PivotError("out_q and q_weight need q")
-    hk = _heads("k", k, k_weight, sh, dtype, dev)
-    hv = None if v is None else _heads("v", v, None, sh, dtype, dev)
-    hq = None if q is None else _heads("q", q, q_weight, sh, dtype, dev)
-    n, page, H = _pages(kpages, vpages, dev, d)
-    if H != Hk or (v is not None and v.shape[-2] != Hk):
-        raise PivotError(f"k and v must have the cache's {H} heads")
-    rope = _rope(freqs, layout, amplitude, eps, d, dev)
-    T, B, g, max_pages, pcu, psl, pbt = _sequences(sh, cu_new, seqlens, block_table, dev, "cu_new")
-    with _On(dev, stream, (k, v, q, kpages, vpages, block_table, seqlens, cu_new, freqs, k_weight, q_weight, out_q)) as raw:
-        pq = None
-        if q is not None:
-            out_q = _like(out_q, q, torch.bfloat16, "out_q")
-            pq = out_q.data_ptr()
-        if T and B:
-            rc = lib.pivot_paged_append(hk, hv, hq, _DTYPES[dtype], rope, pbt, psl, pcu, T, B, d, g, n, page, max_pages,
-                                        kpages.data_ptr(), None if vpages is None else vpages.data_ptr(), pq, raw)
-            if rc:
-                _err(lib, rc)
-    return out_q
+    step = _calls or _load_step()
+    if stream is None:
+        return step.paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new, freqs, layout, amplitude, k_weight, q,
+                                 q_weight, eps, out_q)
+    with _on(stream, k, v, kpages, vpages, block_table, seqlens, cu_new, freqs, k_weight, q, q_weight, out_q):
+        return step.paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new, freqs, layout, amplitude, k_weight, q,
+                                 q_weight, eps, out_q)
 
 
 def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=None, scale=None, include_self=True,
@@ -633,75 +445,26 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
     h // (Hq // Hk).  Token i of n_b sits at position seqlens[b] - n_b + i and sees the keys up to its own, or, with
     include_self=False, those before it (the indexer's keys); a query that sees none gets zeros and lse -inf.
     max_seqlen bounds seqlens; max_q (with cu_q, optional) bounds a sequence's new tokens, which spares a batch of
-    single tokens the launch for longer ones.  scale: d ** -0.5 by default.  out_lse: float32 [..., Hq], the log of each row's sum.
-    Returns bf16 with q's shape."""
-    lib = _lib or load_library()
-    sh, dev = _tokens("q", q)
-    if q.dtype is not torch.bfloat16 or not q.is_contiguous():
-        raise PivotError("q must be a contiguous bfloat16 tensor")
-    d, Hq = sh[-1], sh[-2]
-    n, page, Hk = _pages(kpages, vpages, dev, d)
-    if Hq % Hk or Hq < 1:
-        raise PivotError(f"q's heads must be a multiple of the cache's {Hk} (got {Hq})")
-    T, B, g, max_pages, pcu, psl, pbt = _sequences(sh, cu_q, seqlens, block_table, dev, "cu_q")
-    max_seqlen = int(max_seqlen)
-    if not 1 <= max_seqlen < 1 << 30:
-        raise PivotError(f"max_seqlen must be in [1, 2^30) (got {max_seqlen})")
-    if vpages is None:
-        raise PivotError("paged_attention needs vpages")
-    if max_q is not None and cu_q is not None:
-        if max_q < 1:
-            raise PivotError("max_q must be >= 1")
-        g = int(max_q)
-    opt = _ATTEND(d ** -0.5 if scale is None else scale, 1 if include_self else 0)
-    with _On(dev, stream, (q, kpages, vpages, block_table, seqlens, cu_q, out, out_lse)) as raw:
-        out = _like(out, q, torch.bfloat16, "out")
-        plse = None
-        if out_lse is not None:
-            plse = _out(out_lse, sh[:-1], torch.float32, q.device, "out_lse").data_ptr()
-        if T and B:
-            nbytes = lib.pivot_paged_attention_workspace_size(T, B, Hq, Hk, d, max_seqlen)
-            ws = pws = None
-            if nbytes:
-                ws = q.new_empty(nbytes, dtype=torch.uint8)
-                pws = ws.data_ptr()
-            rc = lib.pivot_paged_attention(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pcu, opt, T, B,
-                                           Hq, Hk, d, g, n, page, max_pages, max_seqlen, out.data_ptr(), plse, pws,
-                                           nbytes, raw)
-            if rc:
-                _err(lib, rc)
-    return out
+    single tokens the launch for longer ones.  scale: d ** -0.5 by default.  out_lse: float32 [..., Hq], the log of each
+    row's sum.  Returns bf16 with q's shape."""
+    step = _calls or _load_step()
+    if stream is None:
+        return step.paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q, scale, include_self, out,
+                                    out_lse, max_q)
+    with _on(stream, q, kpages, vpages, block_table, seqlens, cu_q, out, out_lse):
+        return step.paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q, scale, include_self, out,
+                                    out_lse, max_q)
 
 
 def sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out=None, stream=None):
     """sparse_attention over the paged cache: q bf16 [B, g, H, d], idx int32 [B, g, H, top_k] (the rows of
     pivot_decode_index_paged), kpages and vpages with q's H heads.  Returns float32 [B, g, H, d].  Indices at or
     beyond seqlens[b] and pages outside the cache are left out and reported by sync_status()."""
-    lib = _lib or load_library()
-    sh, dev = _tokens("q", q)
-    if q.dtype is not torch.bfloat16 or not q.is_contiguous():
-        raise PivotError("q must be a contiguous bfloat16 tensor")
-    d, H = sh[-1], sh[-2]
-    n, page, Hk = _pages(kpages, vpages, dev, d)
-    if Hk != H:
-        raise PivotError(f"q must have the cache's {Hk} heads (got {H})")
-    T, B, g, max_pages, _, psl, pbt = _sequences(sh, None, seqlens, block_table, dev, "cu_q")
-    if not isinstance(idx, torch.Tensor) or idx.dim() != 4:
-        raise PivotError("idx must be an int32 tensor [B, g, H, top_k]")
-    if vpages is None:
-        raise PivotError("sparse_attention_paged needs vpages")
-    top_k = idx.shape[3]
-    pidx = _int32("idx", idx, dev, (B, g, H, top_k))
-    with _On(dev, stream, (q, kpages, vpages, block_table, seqlens, idx, out)) as raw:
-        out = _like(out, q, torch.float32, "out")
-        if T and top_k:
-            rc = lib.pivot_sparse_attention_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(), pbt, psl, pidx, B,
-                                                  H, d, g, n, page, max_pages, top_k, out.data_ptr(), raw)
-            if rc:
-                _err(lib, rc)
-        else:
-            out.zero_()
-    return out
+    step = _calls or _load_step()
+    if stream is None:
+        return step.sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out)
+    with _on(stream, q, kpages, vpages, block_table, seqlens, idx, out):
+        return step.sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out)
 
 
 def trace_enable(on: bool = True) -> None:

@@ -1,12 +1,15 @@
-"""Builds the in-tree CUDA library ``libpivot.so`` for sm_100a with nvcc."""
+"""Builds in-tree the CUDA library ``libpivot.so`` for sm_100a with nvcc, and the compiled half of the Python binding
+(``_step``, host code alone) with the host compiler."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpivot.so")
+BINDING = os.path.join(HERE, "_step" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
@@ -18,25 +21,43 @@ def sources():
     return sorted(os.path.join(SRC, f) for f in os.listdir(SRC) if f.endswith((".cu", ".cuh")))
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def stale(target=LIB) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + [os.path.join(ROOT, "include", "pivot.h")]
-    return any(os.path.getmtime(s) > t for s in deps)
+    t = os.path.getmtime(target)
+    deps = [os.path.join(SRC, "binding.cpp")] if target == BINDING else sources()
+    return any(os.path.getmtime(s) > t for s in [*deps, os.path.join(ROOT, "include", "pivot.h")])
+
+
+def _run(cmd, target, verbose):
+    tmp = target + f".tmp{os.getpid()}"
+    cmd = [*cmd, "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, target)
+
+
+def build_binding(verbose: bool = False) -> str:
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+          "-isystem", os.path.join(at, "include"), "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"),
+          os.path.join(SRC, "binding.cpp"), "-L" + os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+          "-ltorch_python"], BINDING, verbose)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return LIB
-    nvcc = os.environ.get("NVCC", "nvcc")
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, os.path.join(SRC, "pivot.cu")]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
+    if force or stale(LIB):
+        nvcc = os.environ.get("NVCC", "nvcc")
+        _run([nvcc, *(["-Xptxas=-v"] if verbose else []), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"),
+              os.path.join(SRC, "pivot.cu")], LIB, verbose)
+    if force or stale(BINDING):
+        build_binding(verbose)
     return LIB
 
 

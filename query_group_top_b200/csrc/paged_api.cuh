@@ -118,6 +118,7 @@ struct PartCost {
   double per_key, fixed, join, join_per_part;
 };
 int best_parts(long long units, long long slots, long long len, const PartCost& c, long long most) {
+  if (most <= 1) return 1;
   long long best = 1;
   double least = -1;
   // the least is at one part or at the most parts of some number of rounds

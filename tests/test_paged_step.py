@@ -5,6 +5,7 @@ roundings allow are in paged_ref.py."""
 import ctypes
 import math
 import os
+import struct
 import subprocess
 
 import numpy as np
@@ -15,6 +16,11 @@ import query_group_top_b200 as qg
 from tests import paged_ref as ref
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+# The C ABI's option structs, packed: pivot_heads_t (data, weight, token_stride, head_stride, heads), pivot_rope_t
+# (freqs, amplitude, eps, rot_dim, layout), pivot_attend_t (scale, include_self).
+PACK_HEADS = struct.Struct("@PPqqi4x").pack
+PACK_ROPE = struct.Struct("@Pddii").pack
+PACK_ATTEND = struct.Struct("@di4x").pack
 
 
 # ------------------------------------------------------------------ without a GPU
@@ -26,7 +32,7 @@ def lib():
 
 
 def heads(p, n=2, ts=256, hs=128, w=None):
-    return qg._HEADS(p, w or 0, ts, hs, n)
+    return PACK_HEADS(p, w or 0, ts, hs, n)
 
 
 @pytest.fixture()
@@ -38,7 +44,7 @@ def ptr():
 
 
 def test_rope_arguments_are_refused_on_the_host(lib, ptr):
-    rope = qg._ROPE(ptr, 1.0, 1e-6, 128, 0)
+    rope = PACK_ROPE(ptr, 1.0, 1e-6, 128, 0)
 
     def call(q=heads(ptr), k=None, dtype=0, pos=ptr, rope=rope, T=4, d=128, oq=ptr, ok=None):
         return lib.pivot_qk_rope(q, k, dtype, pos,
@@ -57,13 +63,13 @@ def test_rope_arguments_are_refused_on_the_host(lib, ptr):
     assert call(q=heads(ptr, hs=4)) == 1
     assert call(oq=ptr + 8) == 1
     for rot in (8, 24, 144, 0, -16):
-        assert call(rope=qg._ROPE(ptr, 1.0, 1e-6, rot, 0)) == 1, rot
-    assert call(rope=qg._ROPE(ptr, 1.0, 1e-6, 64, 2)) == 1              # no such layout
+        assert call(rope=PACK_ROPE(ptr, 1.0, 1e-6, rot, 0)) == 1, rot
+    assert call(rope=PACK_ROPE(ptr, 1.0, 1e-6, 64, 2)) == 1              # no such layout
     assert b"layout" in lib.pivot_last_error()
 
 
 def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
-    rope = qg._ROPE(ptr, 1.0, 1e-6, 128, 0)
+    rope = PACK_ROPE(ptr, 1.0, 1e-6, 128, 0)
 
     def append(k=heads(ptr), v=heads(ptr), q=None, T=4, B=2, d=128, g=2, n=8, page=16, mp=4, kp=ptr, vp=ptr, bt=ptr,
                sl=ptr, cu=None, oq=None):
@@ -96,7 +102,7 @@ def test_append_and_attention_arguments_are_refused_on_the_host(lib, ptr):
     assert attend(T=3) == 1 and attend(g=0) == 1
     assert attend(ms=0) == 1 and attend(ms=1 << 30) == 1
     for s in (0.0, -1.0, math.nan, math.inf):
-        assert attend(opt=qg._ATTEND(s, 1)) == 1, s
+        assert attend(opt=PACK_ATTEND(s, 1)) == 1, s
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, None, 1, 1, 64, 1, 1, 1, 1, 1, ptr, None) == 1
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 64, 1, 1, 1, 1, 0, ptr, None) == 1
     assert lib.pivot_sparse_attention_paged(ptr, ptr, ptr, ptr, ptr, ptr, 1, 1, 32, 1, 1, 1, 1, 1, ptr, None) == 2
@@ -175,8 +181,22 @@ def test_option_structs_are_packed_as_the_header_lays_them_out(tmp_path):
                    '  return 0;\n}\n')
     exe = tmp_path / "sizes"
     subprocess.check_call(["gcc", "-I", os.path.join(ROOT, "include"), "-o", str(exe), str(src)])
-    want = qg._HEADS(1, 2, 3, -4, 5) + qg._ROPE(6, 0.5, 0.25, 7, 8) + qg._ATTEND(0.125, 9)
+    want = PACK_HEADS(1, 2, 3, -4, 5) + PACK_ROPE(6, 0.5, 0.25, 7, 8) + PACK_ATTEND(0.125, 9)
     assert subprocess.check_output([str(exe)]) == want
+
+
+def test_the_binding_refuses_what_is_no_cuda_tensor(lib):
+    """Without a GPU: the compiled half of the binding loads, and tells by the package's own exception."""
+    q = torch.zeros((1, 2, 4, 64), dtype=torch.bfloat16)
+    t, n = torch.zeros((1, 1), dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    pages = torch.zeros((1, 16, 4, 64), dtype=torch.bfloat16)
+    for call in (lambda: qg.paged_attention(q, pages, pages, t, n, 16), lambda: qg.qk_rope(q, None, n, None),
+                 lambda: qg.qk_rope(None, None, None, None), lambda: qg.paged_append(q, q, pages, pages, t, n),
+                 lambda: qg.sparse_attention_paged(q, pages, pages, t, n, t), lambda: qg.paged_append(None, q, pages, pages, t, n),
+                 lambda: qg.qk_rope(7, None, n, None), lambda: qg.paged_attention(q, pages, "pages", t, n, 16),
+                 lambda: qg.paged_attention(q, pages, pages, t, n, "many")):
+        with pytest.raises(qg.PivotError):
+            call()
 
 
 def test_rope_frequencies():
