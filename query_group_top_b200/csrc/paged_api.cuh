@@ -149,20 +149,23 @@ constexpr int kFewRows = 16;   // packed rows of a sequence up to which attend_r
 AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int sms) {
   AttendPlan a{};
   const long long rows = static_cast<long long>(T) * (Hq / Hk);
-  a.min_chunk = 256;
-  const long long most = (max_seqlen + a.min_chunk - 1) / a.min_chunk;
-  const double part_time = static_cast<double>(T) * Hq * d * 8 / 5000;   // a part of every row written and read
-  auto units = [&](long long per_cta) { return (rows + B * per_cta - 1) / (B * per_cta) * B * Hk; };
   // Up to 16 rows a sequence the matrix tiles gain nothing (two sequences of
   // 32000, 8 key heads: 56 us either way); at 24 they take 34 us for 61 (16
   // sequences of 2000).  Many short sequences cost either kernel its CTAs (1500
   // of 120 keys, 20 rows, 8 key heads of 64: 571 us by tiles, 728 by rows).
   a.tiles = rows > static_cast<long long>(kFewRows) * B;
+  // The fewest keys that a part is worth: two key tiles (one: 24 us for 20 at some
+  // sizes, 10 for 12 at others), or two steps of each of the few-row kernel's
+  // warps (4 sequences of 640 keys, 128 heads over 16: 10.3 us; 256 keys: 11.9).
+  a.min_chunk = a.tiles ? 256 : 128;
+  const long long most = (max_seqlen + a.min_chunk - 1) / a.min_chunk;
+  const double part_time = static_cast<double>(T) * Hq * d * 8 / 5000;   // a part of every row written and read
+  auto units = [&](long long per_cta) { return (rows + B * per_cta - 1) / (B * per_cta) * B * Hk; };
   if (a.tiles) {
     // 1.4 us a key tile of both row tiles (1.1 at 64 channels), some 6 us before and after
     a.rows = 256;
     a.nsplit = best_parts(units(256), sms, max_seqlen,
-                          PartCost{(d == 128 ? 1400. : 1100.) / 128, 6000, 6000, part_time}, most);
+                          PartCost{(d == 128 ? 1400. : 1100.) / 128, 6000, 4000, part_time}, most);
   } else {
     // an SM's share of the memory's rate, among its CTAs; some 3 us before and after
     a.rows = rows <= 8ll * B ? 8 : 16;
@@ -243,7 +246,9 @@ int launch_attend(PagedAttendParams ap, const AttendPlan& pl, int most_new, cuda
     TraceScope tr("attend_join", st);
     cudaLaunchConfig_t cfg{};
     const long long rows = static_cast<long long>(ap.rows.T) * ap.Hq;
-    const bool wide = ap.nsplit > 4;
+    // four warps a row only where the rows leave the device room (1694 tokens of
+    // 3 heads of 64 over 5882 keys: 31.6 us with them, 25.2 without)
+    const bool wide = ap.nsplit > 4 && rows <= 1024;
     cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
     cfg.blockDim = dim3(128);
     cfg.stream = st;

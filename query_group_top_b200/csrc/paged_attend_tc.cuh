@@ -551,8 +551,11 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       // moves it by up to 2^-8, which averages out unless a few weights make up the sum; so of every tile the
       // heaviest one's rounding is taken along (error of the 8192-token prefill's output against 64 bits: 0.0018; 0.0023
       // without it; summing every rounded weight as well took 7 % of the time).
-      const float inv = mine > 0 && l != 0.f ? 1.f / (l + dl) : 0.f;
-      const float lse2 = mine > 0 && l != 0.f ? fmaf(m, p.scale_log2, log2f(l)) : neg_inf();
+      // A row that sees no key of the part keeps its reference at -inf; its sum is 0 only up to exp2_poly's
+      // subnormals, over which it would come out NaN (and, though right, worked out key by key: 6 us).
+      const bool sees = mine > 0 && m != neg_inf();
+      const float inv = sees ? 1.f / (l + dl) : 0.f;
+      const float lse2 = sees ? fmaf(m, p.scale_log2, log2f(l)) : neg_inf();
       const long long row = row_ok ? (static_cast<long long>(sp.tok0) + pr / p.grp) * p.Hq + hk * p.grp + pr % p.grp : 0;
       const long long at = static_cast<long long>(split) * p.rows.T * p.Hq + row;
       bool fine = true;
