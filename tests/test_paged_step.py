@@ -927,6 +927,46 @@ def test_calls_on_a_given_stream():
 
 
 @gpu
+def test_calls_from_several_threads_at_once():
+    """Host threads, each with a stream of its own, over one cache (the calls release the interpreter's lock)."""
+    import threading
+    H, d, g, page = 4, 128, 2, 16
+    c = ref.Cache([900, 64, 333], [g] * 3, H, d, page, seed=31)
+    f, _ = qg.rope_frequencies(d)
+    pos = torch.arange(3 * g, dtype=torch.int32, device="cuda")
+    idx = torch.arange(60, dtype=torch.int32, device="cuda").expand(3, g, H, 60).contiguous()
+    qs = [normal((3, g, 2 * H, d), 200 + i) for i in range(4)]
+
+    def calls(q):
+        t, _ = qg.qk_rope(q, None, pos, f)
+        return (t, qg.paged_attention(t, c.kpages, c.vpages, c.table, c.seqlens, c.longest),
+                qg.sparse_attention_paged(t[:, :, :H].contiguous(), c.kpages, c.vpages, c.table, c.seqlens, idx))
+
+    want = [calls(q) for q in qs]
+    torch.cuda.synchronize()
+    wrong, errors = [], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    got = calls(qs[i])
+                    torch.cuda.current_stream().synchronize()
+                    if not all(same_bits(a, b) for a, b in zip(got, want[i])):
+                        wrong.append(i)
+        except Exception as e:       # told by the test below, not lost with the thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(qs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and not wrong
+    assert qg.sync_status() == 0
+
+
+@gpu
 def test_the_binding_refuses():
     c = ref.Cache([30, 5], [2, 2], 2, 64, 16, seed=1)
     q, f = normal((2, 2, 4, 64), 1), qg.rope_frequencies(64)[0]
