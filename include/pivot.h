@@ -296,7 +296,7 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
  * pivot_sparse_attention over a paged cache: q bf16 [B][g][H][d], idx int32
  * [B][g][H][top_k] (the rows of pivot_decode_index_paged), out float32
  * [B][g][H][d].  An index at or beyond seqlens[b], or whose page is not in the
- * cache, is left out and reported.
+ * cache, is left out and reported; a skipped sequence's rows are zeros.
  */
 int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,
                                  const int32_t* seqlens, const int32_t* idx, int B, int H, int d, int g, int num_pages,
@@ -349,9 +349,10 @@ int pivot_decode_index_noalloc(const void* q, const void* kcache, const int32_t*
 /*
  * Synchronises `stream`, then reads and clears this device's kernel status
  * word.  Returns PIVOT_OK, PIVOT_ERR_TIMEOUT (a bounded wait inside a kernel
- * gave up; that call's outputs are not valid), PIVOT_ERR_INVALID_ARG (a decode
- * sequence exceeded max_seqlen, or status bit 16: a page outside the cache or an
- * index outside its sequence) or PIVOT_ERR_CUDA (a CUDA error, or status bit
+ * gave up; that call's outputs are not valid), PIVOT_ERR_INVALID_ARG (status bit
+ * 2: a sequence exceeded max_seqlen or its block table, held fewer rows than its
+ * new tokens, or had offsets that do not fit; or bit 16: a page outside the cache
+ * or an index outside its sequence) or PIVOT_ERR_CUDA (a CUDA error, or status bit
  * 8: a refine selection exceeded its round limit, which finite scores never
  * do; that call's outputs are not valid).  *flags (nullable) receives the raw
  * status bits; bit 4 means some rows took the exact fallback path (results

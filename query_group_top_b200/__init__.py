@@ -459,7 +459,8 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
 def sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out=None, stream=None):
     """sparse_attention over the paged cache: q bf16 [B, g, H, d], idx int32 [B, g, H, top_k] (the rows of
     pivot_decode_index_paged), kpages and vpages with q's H heads.  Returns float32 [B, g, H, d].  Indices at or
-    beyond seqlens[b] and pages outside the cache are left out and reported by sync_status()."""
+    beyond seqlens[b] and pages outside the cache are left out, sequences whose seqlens do not fit (fewer than g, more
+    than the table covers) get zeros; both are reported by sync_status()."""
     step = _calls or _load_step()
     if stream is None:
         return step.sparse_attention_paged(q, kpages, vpages, block_table, seqlens, idx, out)

@@ -53,10 +53,12 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
   const int rank = static_cast<int>(blockIdx.x % p.parts); // the CTA's rank in its cluster
   const int h = static_cast<int>(rh % p.H);
   const int b = static_cast<int>(rh / p.H / p.g);
-  const int len = min(p.rows.seqlens[b], p.rows.max_len);
+  const NewSpan sp = p.rows.span(b);
+  if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
+  const int len = sp.len;
   const int chunk = ((p.top_k + p.parts - 1) / p.parts + 15) & ~15;
   const int tbeg = rank * chunk;
-  int tend = min(p.top_k, tbeg + chunk);
+  int tend = sp.ok ? min(p.top_k, tbeg + chunk) : tbeg;    // a sequence that does not fit gets zeros
   const int32_t* row = p.idx + static_cast<long long>(rh) * p.top_k;
   R kv;
   kv.init(smem, p.kpages, p.vpages, p.H, h, warp, lane);
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
   } else if (warp == 0) {
     float e[D / 32], lse2;
     attend_row_exact<D>(
-        p, p.H, h, rh, 0, p.top_k,
+        p, p.H, h, rh, 0, sp.ok ? p.top_k : 0,
         [&](int t) {
           const int j = __ldg(row + t);
           return j >= 0 && j < len ? rows.row(j) : -1;

@@ -856,7 +856,9 @@ int pivot_sync_status(void* stream, int* flags) {
   CUDA_TRY(cudaMemcpy(dev->status, &zero, sizeof zero, cudaMemcpyHostToDevice));
   if (flags) *flags = v;
   if (v & kStTimeout) return fail(PIVOT_ERR_TIMEOUT, "a kernel wait timed out; outputs of that call are invalid");
-  if (v & kStBadLen) return fail(PIVOT_ERR_INVALID_ARG, "a decode sequence was longer than max_seqlen");
+  if (v & kStBadLen)
+    return fail(PIVOT_ERR_INVALID_ARG,
+                "a sequence was longer than max_seqlen or its block table, shorter than its new tokens, or had offsets that do not fit");
   if (v & kStBadPage)
     return fail(PIVOT_ERR_INVALID_ARG, "a block table named a page outside the cache, or an index a row outside its sequence");
   if (v & kStNoConverge) return fail(PIVOT_ERR_CUDA, "a refine selection did not converge; outputs of that call are invalid");

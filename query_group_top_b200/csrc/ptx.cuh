@@ -13,7 +13,7 @@ namespace pivot {
 // Device status bits, OR-ed into the library's per-device status word.
 enum : int {
   kStTimeout = 1,   // a bounded wait on a barrier gave up
-  kStBadLen = 2,    // a decode sequence was longer than the declared maximum
+  kStBadLen = 2,    // a sequence was longer than the declared maximum or its table, or its lengths contradict each other
   kStFallback = 4,  // informational: some rows took the exact fallback path
   kStNoConverge = 8,  // a selection exceeded its round limit (cannot happen on finite scores)
   kStBadPage = 16,    // a block table named a page outside the cache, or an index a row outside its sequence
