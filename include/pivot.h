@@ -214,6 +214,7 @@ int pivot_decode_index_paged(const void* q, const void* kpages, const int32_t* b
 /* Type of a call's inputs, and how a rotation pairs the first rot_dim channels:
  * (i, i + rot_dim/2), or (2i, 2i+1). */
 typedef enum { PIVOT_BF16 = 0, PIVOT_FP16 = 1, PIVOT_FP32 = 2 } pivot_dtype_t;
+#define PIVOT_CLEAR_LEFT_OUT 0x100 /* option bit of pivot_paged_append's dtype */
 typedef enum { PIVOT_ROPE_HALF = 0, PIVOT_ROPE_INTERLEAVED = 1 } pivot_rope_layout_t;
 
 /* Head rows [T][heads][d] of new tokens, strides in elements (each row must
@@ -256,9 +257,12 @@ int pivot_qk_rope(const pivot_heads_t* q, const pivot_heads_t* k, int dtype, con
  * Writes the new keys (normed and rotated as above, at their rows' positions)
  * and values (NULL: a cache of keys alone) into their pages, and, where q is
  * given, norms and rotates the tokens' queries into out_q (bf16 [T][heads][d],
- * contiguous; it may be q itself, as above) in the same launch.  The new tokens' rows must be in pages of their own: two
- * sequences that write the same row race.  A skipped sequence's rows and queries
- * are left as they were.
+ * contiguous; it may be q itself, as above) in the same launch.  The new tokens'
+ * rows must be in pages of their own: two sequences that write the same row race.
+ * A token of a skipped sequence, and one whose page is not in the cache, is left
+ * out: neither its row nor its queries are written.  With PIVOT_CLEAR_LEFT_OUT
+ * in dtype the queries of such tokens, and of those behind cu_new[B], become zeros
+ * (for an out_q that holds nothing yet).
  */
 int pivot_paged_append(const pivot_heads_t* k, const pivot_heads_t* v, const pivot_heads_t* q, int dtype,
                        const pivot_rope_t* rope, const int32_t* block_table, const int32_t* seqlens,

@@ -425,8 +425,9 @@ def paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new=None, freqs=
     keys alone; q None: no queries.  kpages, vpages: bf16 [num_pages, page_size, heads, d], written in place.
     block_table int32 [B, max_pages]; seqlens int32 [B]: each sequence's rows with the new ones, the same that the
     indexer and the attention then take: token i of n_b goes to row seqlens[b] - n_b + i.  Returns the queries in
-    bf16 (None without q).  Sequences that do not fit their table and pages outside the cache are left out and
-    reported by sync_status()."""
+    bf16 (None without q).  Sequences that do not fit their table and tokens whose page is outside the cache are left
+    out and reported by sync_status(); their queries, and those of tokens behind cu_new[B], are zeros, or what out_q
+    held where it is given."""
     step = _calls or _load_step()
     if stream is None:
         return step.paged_append(k, v, kpages, vpages, block_table, seqlens, cu_new, freqs, layout, amplitude, k_weight, q,

@@ -344,13 +344,15 @@ PyObject* paged_append(PyObject* const* a) {
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(t.dev));
   Output oq;
   if (q) oq.make("out_q", a[14], q->sizes(), at::kBFloat16, *q);
+  const bool fresh = q && a[14] == Py_None;   // tokens that are left out have zeros in it, not what the memory held
+  if (fresh && !s.B) oq.t.zero_();
   if (s.T && s.B) {
     const cudaStream_t st = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(t.dev)).stream();
     void *const kp = kpages.data_ptr(), *const vp = vpages ? vpages->data_ptr() : nullptr;
     int rc;
     {
       NoGil free;
-      rc = lib.paged_append(&hk, v ? &hv : nullptr, q ? &hq : nullptr, dtype, &rope, s.table, s.seqlens, s.cu, s.T, s.B, t.d,
+      rc = lib.paged_append(&hk, v ? &hv : nullptr, q ? &hq : nullptr, fresh ? dtype | PIVOT_CLEAR_LEFT_OUT : dtype, &rope, s.table, s.seqlens, s.cu, s.T, s.B, t.d,
                             s.g, pg.n, pg.size, s.max_pages, kp, vp, oq.data, st);
     }
     check(rc);

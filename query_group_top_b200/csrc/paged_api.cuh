@@ -321,6 +321,8 @@ int pivot_paged_append(const pivot_heads_t* k, const pivot_heads_t* v, const piv
                        const int32_t* cu_new, int T, int B, int d, int g, int num_pages, int page_size, int max_pages,
                        void* kpages, void* vpages, void* out_q, void* stream) {
   RopeParams rp{};
+  rp.clear = (dtype & PIVOT_CLEAR_LEFT_OUT) != 0;
+  dtype &= ~PIVOT_CLEAR_LEFT_OUT;
   if (int rc = check_dtype(dtype)) return rc;
   if (!k || !kpages || (v && !vpages) || (q && !out_q)) return fail(PIVOT_ERR_INVALID_ARG, "null tensor pointer");
   if (int rc = head_rows("k", k, dtype, &rp.k)) return rc;

@@ -52,6 +52,7 @@ struct RopeParams {
   PagedRows rows;           // paged: where the tokens' rows lie
   int T, rot, tokens_per_block;
   float amplitude, eps;
+  bool clear;               // paged: queries of tokens that are left out become zeros, else they stay
   int* status;
 };
 
@@ -220,7 +221,9 @@ __global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 7 : 6) rope_kernel(c
     }
   }
   // One kind's rows: src from row0 on, to dst + head * D; next: the first row of the kind behind it.
-  auto walk = [&](const HeadRows& src, const T* row0, uint16_t* dst, bool turn, const float4 (*w)[LG], const T* next) {
+  // put: the token's rows are written, as zeros where it is left out.
+  auto walk = [&](const HeadRows& src, const T* row0, uint16_t* dst, bool put, bool turn, const float4 (*w)[LG],
+                  const T* next) {
     const long long step = gpt * src.head_stride;
     const T* at = row0;
     dst += g * D;
@@ -278,15 +281,20 @@ __global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 7 : 6) rope_kernel(c
           unpair_f32(b[c], f[4 * c + 1], f[4 * c + 3]);
         }
       }
-      if (row >= 0 && h < src.n) {
+      if (put && h < src.n) {
+        if (row < 0) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] = 0.f;
+        }
         store8_bf16(dst + ca, f);
         store8_bf16(dst + cb, f + 8);
       }
     }
   };
-  if (q0) walk(p.q, q0, p.out_q + t * p.q.n * D, turns, w_s[0], k0);
-  if (k0) walk(p.k, k0, paged ? p.kpages + row * p.k.n * D : p.out_k + t * p.k.n * D, turns, w_s[1], v0);
-  if (v0) walk(p.v, v0, p.vpages + row * p.v.n * D, false, nullptr, nullptr);
+  const bool in = row >= 0;
+  if (q0) walk(p.q, q0, p.out_q + t * p.q.n * D, in || (p.clear && tok < nt), turns, w_s[0], k0);
+  if (k0) walk(p.k, k0, paged ? p.kpages + row * p.k.n * D : p.out_k + t * p.k.n * D, in, turns, w_s[1], v0);
+  if (v0) walk(p.v, v0, p.vpages + row * p.v.n * D, in, false, nullptr, nullptr);
 }
 
 }  // namespace pivot

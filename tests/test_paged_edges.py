@@ -44,3 +44,41 @@ def test_index_rows_of_a_sequence_that_does_not_fit(top_k, d):
         assert status()[0] == qg.FLAG_BADLEN, wrong
         assert bool((out[1] == 0).all()), wrong
         assert same_bits(out[0], good[0]) and same_bits(out[2], good[2])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_gives_zeros_for_the_queries_of_tokens_left_out(d, dtype):
+    """Queries that the call allocates hold a result or zeros, never what the memory held: a page outside the cache, a
+    length that does not fit, tokens behind the last sequence, no sequence at all."""
+    H, Hq, page = 2, 5, 16
+    c = ref.Cache([20, 3, 40, 9], [4] * 4, H, d, page, seed=42)
+    k, v, q = normal((19, H, d), 43, dtype), normal((19, H, d), 44, dtype), normal((19, Hq, d), 45, dtype)
+    f, _ = qg.rope_frequencies(d)
+    good = qg.paged_append(k, v, c.kpages.clone(), c.vpages.clone(), c.table, c.seqlens, cu_new=c.cu, freqs=f, q=q)
+    assert status()[0] == 0 and bool((good[16:] == 0).all()) and bool(good[:16].any(-1).all())
+    table, lens = c.table.clone(), c.seqlens.clone()
+    table[0, 1] = c.kpages.shape[0]          # rows 16.. of sequence 0
+    lens[2] = 3                              # fewer rows than new tokens
+    for ragged in (True, False):
+        n = 19 if ragged else 16
+        shape = (lambda x: x) if ragged else (lambda x: x[:16].view(4, 4, *x.shape[1:]))  # noqa: E731
+        junk = torch.full((n, Hq, d), math.nan, dtype=torch.bfloat16, device="cuda")
+        del junk                             # the allocator hands this memory out again
+        out = qg.paged_append(shape(k), shape(v), c.kpages.clone(), c.vpages.clone(), table, lens,
+                              cu_new=c.cu if ragged else None, freqs=f, q=shape(q)).view(n, Hq, d)
+        assert status()[0] == qg.FLAG_BADLEN | qg.FLAG_BADPAGE
+        want = good[:n].clone()
+        want[0:4], want[8:12] = 0, 0
+        assert same_bits(out, want)
+        mine = torch.full((n, Hq, d), 9.0, dtype=torch.bfloat16, device="cuda")
+        qg.paged_append(shape(k), shape(v), c.kpages.clone(), c.vpages.clone(), table, lens,
+                        cu_new=c.cu if ragged else None, freqs=f, q=shape(q), out_q=mine.view(shape(q).shape))
+        status()
+        want[0:4], want[8:12], want[16:] = 9, 9, 9
+        assert same_bits(mine, want)
+    junk = torch.full((19, Hq, d), math.nan, dtype=torch.bfloat16, device="cuda")
+    del junk
+    none = qg.paged_append(k, v, c.kpages.clone(), c.vpages.clone(), c.table[:0], c.seqlens[:0], cu_new=c.cu[:1], freqs=f, q=q)
+    assert bool((none == 0).all())
