@@ -171,6 +171,12 @@ __global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 7 : 6) rope_kernel(c
     }
   }
 
+  // lengths that do not fit are told of every sequence, those without new tokens too
+  if (paged) {
+    for (long long b = static_cast<long long>(blockIdx.x) * kRopeNT + threadIdx.x; b < p.rows.B;
+         b += static_cast<long long>(gridDim.x) * kRopeNT)
+      if (!p.rows.span(static_cast<int>(b)).ok) atomicOr(p.status, kStBadLen);
+  }
   for (int i = warp; i < nt; i += kRopeNT / 32) {
     const int ti = t0 + i;
     int pos = 0;
@@ -184,11 +190,7 @@ __global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 7 : 6) rope_kernel(c
         if (s.ok) {
           row = p.rows.row(b, pos);
           if (row < 0 && lane == 0) atomicOr(p.status, kStBadPage);
-        } else if (lane == 0) {
-          atomicOr(p.status, kStBadLen);
         }
-      } else if (!s.ok && lane == 0) {
-        atomicOr(p.status, kStBadLen);
       }
     } else if (p.rot) {
       pos = p.positions[ti];

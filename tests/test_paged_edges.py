@@ -82,3 +82,27 @@ def test_append_gives_zeros_for_the_queries_of_tokens_left_out(d, dtype):
     del junk
     none = qg.paged_append(k, v, c.kpages.clone(), c.vpages.clone(), c.table[:0], c.seqlens[:0], cu_new=c.cu[:1], freqs=f, q=q)
     assert bool((none == 0).all())
+
+
+@gpu
+@pytest.mark.parametrize("where", [0, 1, 150, 599])
+def test_append_tells_of_lengths_that_do_not_fit_in_sequences_without_new_tokens(where):
+    """As the attention does over the same arrays; the tokens of the others are written all the same."""
+    new = [0] * 600
+    new[3], new[400] = 5, 1                  # six tokens, so the launch has far fewer blocks than the batch sequences
+    held = [i % 30 for i in range(600)]
+    c = ref.Cache(held, new, 1, 64, 16, seed=46)
+    k = normal((6, 1, 64), 47)
+    q = normal((6, 1, 64), 48)
+    want = c.kpages.clone(), c.vpages.clone()
+    qg.paged_append(k, k, *want, c.table, c.seqlens, cu_new=c.cu)
+    assert status()[0] == 0
+    for wrong in (-1, c.table.shape[1] * c.page + 1):
+        lens = c.seqlens.clone()
+        lens[where] = wrong
+        got = c.kpages.clone(), c.vpages.clone()
+        qg.paged_append(k, k, *got, c.table, lens, cu_new=c.cu)
+        assert status()[0] == qg.FLAG_BADLEN
+        assert same_bits(got[0], want[0]) and same_bits(got[1], want[1])
+        qg.paged_attention(q, *got, c.table, lens, 4096, cu_q=c.cu)
+        assert status()[0] == qg.FLAG_BADLEN
