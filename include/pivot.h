@@ -298,8 +298,8 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
 
 /*
  * pivot_sparse_attention over a paged cache: q bf16 [B][g][H][d], idx int32
- * [B][g][H][top_k] (the rows of pivot_decode_index_paged), out float32
- * [B][g][H][d].  An index at or beyond seqlens[b], or whose page is not in the
+ * [B][g][H][top_k] (the rows of pivot_decode_index_paged; top_k at most 2^30), out
+ * float32 [B][g][H][d].  An index at or beyond seqlens[b], or whose page is not in the
  * cache, is left out and reported; a skipped sequence's rows are zeros.
  */
 int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,

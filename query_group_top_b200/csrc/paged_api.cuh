@@ -401,6 +401,8 @@ int pivot_sparse_attention_paged(const void* q, const void* kpages, const void* 
     return fail(PIVOT_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
   if (d != 64 && d != 128) return fail(PIVOT_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", d);
   if (B < 1 || g < 1 || H < 1 || top_k < 1) return fail(PIVOT_ERR_INVALID_ARG, "need B, g, H, top_k >= 1");
+  // places in a row are counted in 32 bits, a CTA's stride past the last one included
+  if (top_k > (1 << 30)) return fail(PIVOT_ERR_INVALID_ARG, "top_k must be at most 2^30 (got %d)", top_k);
   if (static_cast<double>(B) * g * H >= 2147483648.0) return fail(PIVOT_ERR_INVALID_ARG, "B * g * H too large");
   AttendPagedParams ap{};
   if (int rc = paged_rows(block_table, seqlens, nullptr, B * g, B, g, num_pages, page_size, max_pages, 0x7FFFFFFF, &ap.rows))

@@ -22,6 +22,19 @@ def status():
     return flags.value, (lib.pivot_last_error().decode() if rc else "")
 
 
+# ------------------------------------------------------------------ without a GPU
+def test_index_rows_longer_than_their_places_count_are_refused():
+    """Near 2^31 places a walk in 32 bits would pass its end: refused before any device is asked for."""
+    from query_group_top_b200 import build
+    build.build()
+    lib = qg.load_library()
+    buf = ctypes.create_string_buffer(64)
+    p = ctypes.addressof(buf) + (-ctypes.addressof(buf)) % 16
+    for top_k in ((1 << 30) + 1, 2**31 - 200, 2**31 - 1):
+        assert lib.pivot_sparse_attention_paged(p, p, p, p, p, p, 1, 1, 64, 1, 1, 16, 1, top_k, p, None) == 1
+        assert b"top_k" in lib.pivot_last_error()
+
+
 # ------------------------------------------------------------------ sequences that do not fit
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
