@@ -171,12 +171,11 @@ __global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 7 : 6) rope_kernel(c
     }
   }
 
-  // lengths that do not fit are told of every sequence, those without new tokens too
-  if (paged) {
-    for (long long b = static_cast<long long>(blockIdx.x) * kRopeNT + threadIdx.x; b < p.rows.B;
-         b += static_cast<long long>(gridDim.x) * kRopeNT)
-      if (!p.rows.span(static_cast<int>(b)).ok) atomicOr(p.status, kStBadLen);
-  }
+  // lengths that do not fit are told of every sequence, those without new tokens too; at the end, the first ones'
+  // being on their way from here
+  const long long b0 = static_cast<long long>(blockIdx.x) * kRopeNT + threadIdx.x;
+  NewSpan told{0, 0, 0, true};
+  if (paged && b0 < p.rows.B) told = p.rows.span(static_cast<int>(b0));
   for (int i = warp; i < nt; i += kRopeNT / 32) {
     const int ti = t0 + i;
     int pos = 0;
@@ -297,6 +296,10 @@ __global__ void __launch_bounds__(kRopeNT, sizeof(T) == 2 ? 7 : 6) rope_kernel(c
   if (q0) walk(p.q, q0, p.out_q + t * p.q.n * D, in || (p.clear && tok < nt), turns, w_s[0], k0);
   if (k0) walk(p.k, k0, paged ? p.kpages + row * p.k.n * D : p.out_k + t * p.k.n * D, in, turns, w_s[1], v0);
   if (v0) walk(p.v, v0, p.vpages + row * p.v.n * D, in, false, nullptr, nullptr);
+  for (long long b = b0 + static_cast<long long>(gridDim.x) * kRopeNT; paged && b < p.rows.B;
+       b += static_cast<long long>(gridDim.x) * kRopeNT)
+    if (!p.rows.span(static_cast<int>(b)).ok) atomicOr(p.status, kStBadLen);
+  if (!told.ok) atomicOr(p.status, kStBadLen);
 }
 
 }  // namespace pivot
