@@ -42,6 +42,41 @@ struct AttendPagedParams {
   int* status;
 };
 
+// A row that came out not finite (paged_attend.cuh): thread c has channel c's value and gets it anew.  By the whole CTA;
+// kinds: D words of shared memory.
+template <int D>
+__device__ __noinline__ float sparse_row_not_finite(const AttendPagedParams& p, unsigned rh, int h, const int32_t* row,
+                                                    const SequenceRows rows, int len, float value, uint32_t* kinds) {
+  constexpr int NW = KvRing<D>::NW, C = D / 32;
+  const int c = threadIdx.x, warp = c >> 5, lane = c & 31;
+  auto cache_row = [&](int t) {
+    const int j = __ldg(row + t);
+    return j >= 0 && j < len ? rows.row(j) : -1;
+  };
+  if (c < D) kinds[c] = 0;   // of a channel's values: bit 0 infinite, 1 its negative, 2 NaN
+  __syncthreads();
+  FirstNonFinite<D> odd;
+  const int share = (p.top_k + NW - 1) / NW;
+  odd.look(p, p.H, h, warp * share, min(p.top_k, (warp + 1) * share), cache_row, lane);
+#pragma unroll
+  for (int x = 0; x < C; ++x) {
+    const uint32_t k = (odd.pos[x] != odd.NONE ? 1u : 0u) | (odd.neg[x] != odd.NONE ? 2u : 0u) | (odd.nan[x] != odd.NONE ? 4u : 0u);
+    if (k) atomicOr(&kinds[lane * C + x], k);
+  }
+  __syncthreads();
+  const uint32_t k = c < D ? kinds[c] : 0u;
+  if (k) value = __int_as_float(k == 1u ? 0x7f800000 : k == 2u ? 0xff800000 : 0x7fffffff);
+  if (!__syncthreads_or(!k && !finite(value))) return value;
+  if (warp == 0) {
+    float o[C], lse2;
+    attend_row_exact<D>(p, p.H, h, rh, 0, p.top_k, cache_row, lane, o, &lse2);
+#pragma unroll
+    for (int x = 0; x < C; ++x) kinds[lane * C + x] = __float_as_uint(o[x]);
+  }
+  __syncthreads();
+  return c < D ? __uint_as_float(kinds[c]) : 0.f;
+}
+
 template <int D>
 __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __grid_constant__ AttendPagedParams p) {
   using R = KvRing<D>;
@@ -54,11 +89,10 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
   const int h = static_cast<int>(rh % p.H);
   const int b = static_cast<int>(rh / p.H / p.g);
   const NewSpan sp = p.rows.span(b);
-  if (!sp.ok && threadIdx.x == 0) atomicOr(p.status, kStBadLen);
-  const int len = sp.len;
+  const int len = sp.ok ? sp.len : 0;                      // a sequence that does not fit gets zeros
   const int chunk = ((p.top_k + p.parts - 1) / p.parts + 15) & ~15;
   const int tbeg = rank * chunk;
-  int tend = sp.ok ? min(p.top_k, tbeg + chunk) : tbeg;    // a sequence that does not fit gets zeros
+  int tend = min(p.top_k, tbeg + chunk);
   const int32_t* row = p.idx + static_cast<long long>(rh) * p.top_k;
   R kv;
   kv.init(smem, p.kpages, p.vpages, p.H, h, warp, lane);
@@ -86,7 +120,7 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
   auto place = [&](int j) -> int {
     if (j < 0) return -1;
     const int at = j < len ? rows.row(j) : -1;
-    if (at < 0) atomicOr(p.status, kStBadPage);
+    if (at < 0 && sp.ok) atomicOr(p.status, kStBadPage);
     return at;
   };
   int next = place(entry(0));
@@ -202,22 +236,12 @@ __global__ void __launch_bounds__(128) sparse_attention_paged_kernel(const __gri
     cluster.sync();   // no CTA leaves while its part is being read
   }
   if (rank > 0) return;
-  const float value = cl == 0.f ? 0.f : acc / cl;          // 0 in threads without a channel
+  if (!sp.ok && c == 0) atomicOr(p.status, kStBadLen);     // told here: at the start the whole row would wait for the length
+  float value = cl == 0.f ? 0.f : acc / cl;                // 0 in threads without a channel
   // an infinite value under a weight whose lower terms are zero came in as 0 * inf
-  if (!__syncthreads_or(!(fabsf(value) < __int_as_float(0x7f800000)))) {
-    if (c < D) p.out[static_cast<long long>(rh) * D + c] = value;
-  } else if (warp == 0) {
-    float e[D / 32], lse2;
-    attend_row_exact<D>(
-        p, p.H, h, rh, 0, sp.ok ? p.top_k : 0,
-        [&](int t) {
-          const int j = __ldg(row + t);
-          return j >= 0 && j < len ? rows.row(j) : -1;
-        },
-        lane, e, &lse2);
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) p.out[static_cast<long long>(rh) * D + lane * (D / 32) + x] = e[x];
-  }
+  if (__syncthreads_or(!finite(value) && cl == cl))
+    value = sparse_row_not_finite<D>(p, rh, h, row, SequenceRows(p.rows, b), len, value, reinterpret_cast<uint32_t*>(co));
+  if (c < D) p.out[static_cast<long long>(rh) * D + c] = value;
 }
 
 }  // namespace pivot

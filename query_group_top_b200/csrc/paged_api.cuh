@@ -364,7 +364,8 @@ int pivot_paged_attention(const void* q, const void* kpages, const void* vpages,
   if (max_seqlen >= (1 << 30)) return fail(PIVOT_ERR_INVALID_ARG, "max_seqlen too large");
   const double scale = options ? options->scale : 1.0 / sqrt(static_cast<double>(d));
   if (!(scale > 0.0) || !(scale < 1e30)) return fail(PIVOT_ERR_INVALID_ARG, "scale must be positive and finite");
-  if (static_cast<long long>(T) * (Hq / Hk) >= (1ll << 31) - 32) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
+  // rows of q are counted in 32 bits (more than 180 GB of them would pass that)
+  if (static_cast<long long>(T) * Hq >= (1ll << 31) - 512) return fail(PIVOT_ERR_INVALID_ARG, "too many rows");
   DeviceInfo* dev = nullptr;
   if (int rc = device_info(&dev)) return rc;
   const AttendPlan pl = plan_attend(T, B, Hq, Hk, d, max_seqlen, dev->sms);

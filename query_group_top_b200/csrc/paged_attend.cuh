@@ -130,45 +130,190 @@ __device__ __forceinline__ int locate_tile(const PagedAttendParams& a, int rows,
   return -1;
 }
 
+// ------------------------------------------------------------------ rows that are not finite
+// By definition an infinity or NaN among the values that a row sees makes its
+// channel so, however small its weight, and one that it does not see leaves it
+// alone.  A product over a whole tile does neither by itself: there a value that
+// is not seen meets a weight of zero, and a small weight may round to zero.  So
+//  * values that some row of a tile does not see are made finite (zeros) where the
+//    tile lies in shared memory (cleaned), which costs the last tiles alone;
+//  * if that found any, or a row came out not finite though the sum of its weights
+//    is (a NaN there is the row's), FirstNonFinite looks the values up and puts in
+//    what the row's channels have to be;
+//  * what is still not finite had values so large that a sum went past the type's
+//    end: attend_row_exact works that row out anew.
+// One infinite value at the start of a 4096-token prefill of 16 heads so takes
+// 295 us for the 83 without it; every later row key by key took 69 ms.
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __int_as_float(0x7f800000); }
+__device__ __forceinline__ float add_weighted(float w, float v, float sum) { return finite(v) ? fmaf(w, v, sum) : sum + v; }
+
+// acc, zero so far, and not zero from the first pair of bf16 values on that is not
+// finite (0 times it is NaN).
+__device__ __forceinline__ uint32_t odd_so_far(uint32_t acc, uint32_t two) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(two), "r"(0u));
+  return acc;
+}
+__device__ __forceinline__ uint32_t odd_so_far(uint32_t acc, const uint4& v) {
+  return odd_so_far(odd_so_far(odd_so_far(odd_so_far(acc, v.x), v.y), v.z), v.w);
+}
+// Eight bf16 values, those that are not finite made zero.
+__device__ __forceinline__ uint4 cleaned(uint4 v) {
+  auto two = [](uint32_t w) {
+    const uint32_t odd = ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;   // an exponent of all ones carries
+    return w & ~((odd >> 15) * 0xFFFFu);
+  };
+  return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+}
+
+// A lane's D/32 channels [lane * D/32, ...) of a row of keys or values.
+template <int D>
+__device__ __forceinline__ void load_lane(const uint16_t* row, int lane, uint32_t (&w)[D / 64]) {
+  if constexpr (D == 128) {
+    const uint2 u = *reinterpret_cast<const uint2*>(row + lane * 4);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(row + lane * 2);
+  }
+}
+
+// The first keys whose value is +infinity, -infinity and NaN in each of a lane's channels.
+template <int D>
+struct FirstNonFinite {
+  static constexpr int C = D / 32, NONE = 0x7FFFFFFF;
+  int pos[C], neg[C], nan[C];
+
+  // Looks through the values of the keys j0 <= j < j1, by a whole warp; row_of as below.
+  template <class P, class RowOf>
+  __device__ __forceinline__ void look(const P& p, int heads, int head, int j0, int j1, RowOf row_of, int lane) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) pos[c] = neg[c] = nan[c] = NONE;
+    for (int jb = j0; jb < j1; jb += 32) {
+      const int mine = jb + lane < j1 ? static_cast<int>(row_of(jb + lane)) : -1;
+      for (int x0 = 0; x0 < 32; x0 += 8) {
+        uint32_t w[8][D / 64], odd = 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int row = __shfl_sync(0xffffffffu, mine, x0 + x);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) w[x][h] = 0;
+          if (row >= 0) load_lane<D>(p.vpages + (static_cast<long long>(row) * heads + head) * D, lane, w[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) odd = odd_so_far(odd, w[x][h]);
+        if (!odd) continue;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const uint32_t v = w[x][c / 2] >> (16 * (c & 1)) & 0xFFFFu;
+            const int j = jb + x0 + x;
+            pos[c] = min(pos[c], v == 0x7F80u ? j : NONE);
+            neg[c] = min(neg[c], v == 0xFF80u ? j : NONE);
+            nan[c] = min(nan[c], (v & 0x7FFFu) > 0x7F80u ? j : NONE);
+          }
+      }
+    }
+  }
+  // What channel c of a row that sees the keys below lim has to be: not finite, or 0 where it may be finite.
+  __device__ __forceinline__ float due(int c, int lim) const {
+    const bool up = pos[c] < lim, down = neg[c] < lim;
+    if (nan[c] < lim || (up && down)) return __int_as_float(0x7fffffff);
+    return up ? __int_as_float(0x7f800000) : down ? __int_as_float(0xff800000) : 0.f;
+  }
+  // Puts what has to be not finite into a row's channels; true where another one is not finite.
+  __device__ __forceinline__ bool settle(float (&o)[C], int lim) const {
+    bool open = false;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float x = due(c, lim);
+      if (x != 0.f)
+        o[c] = x;
+      else
+        open = open || !finite(o[c]);
+    }
+    return __any_sync(0xffffffffu, open);
+  }
+};
+
 // One query row over the keys j0 <= j < j1, key j in cache row row_of(j) (-1:
-// left out, -2: zeros), by a whole warp, key after key, reading only those keys: lane l holds
-// channels [l * D/32, ...).  For rows whose tile gave a value that is not
-// finite: there a masked position's infinity or NaN, or a weight's part that
-// rounds to zero, may have come in as 0 * inf, and here it does not.
+// left out, -2: zeros), by a whole warp, reading only those keys: 32 at a time, a
+// key a lane for the scores, then lane l with channels [l * D/32, ...) for the values.
+// The weights are taken times kDown, so that no sum of values ends past the type's end.
+constexpr float kDown = 0x1p-31f, kUp = 0x1p31f;
 template <int D, class P, class RowOf>
 __device__ __forceinline__ void attend_row_exact(const P& p, int heads, int head, long long qrow, int j0, int j1,
-                                              RowOf row_of, int lane, float (&o)[D / 32], float* lse2) {
+                                                 RowOf row_of, int lane, float (&o)[D / 32], float* lse2) {
   constexpr int C = D / 32;
-  float q[C], m = neg_inf(), l = 0.f;
+  using Bf16 = __nv_bfloat16;
+  const Bf16* const q = reinterpret_cast<const Bf16*>(p.q + qrow * D);
+  float m = neg_inf(), l = 0.f;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    q[c] = __uint_as_float(static_cast<uint32_t>(p.q[qrow * D + lane * C + c]) << 16);
-    o[c] = 0.f;
-  }
-  for (int j = j0; j < j1; ++j) {
-    const long long row = row_of(j);
-    if (row == -1) continue;
-    const long long at = (row * heads + head) * D + lane * C;
+  for (int c = 0; c < C; ++c) o[c] = 0.f;
+  for (int jb = j0; jb < j1; jb += 32) {
+    const int mine = jb + lane < j1 ? static_cast<int>(row_of(jb + lane)) : -1;
     float s = 0.f;
+    if (mine >= 0) {
+      const Bf16* const k = reinterpret_cast<const Bf16*>(p.kpages + (static_cast<long long>(mine) * heads + head) * D);
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        Vec8<Bf16> vk, vq;
+        float fk[8], fq[8];
+        vk.load(k + 8 * c);
+        vq.load(q + 8 * c);
+        vk.get(fk);
+        vq.get(fq);
 #pragma unroll
-    for (int c = 0; c < C; ++c) s = fmaf(q[c], row < 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(p.kpages[at + c]) << 16), s);
+        for (int x = 0; x < 8; ++x) s = fmaf(fk[x], fq[x], s);
+      }
+    }
+    s = mine == -1 ? neg_inf() : s * p.scale_log2;
+    float mn = s;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s);
+    for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+    mn = fmaxf(m, mn);
     const float ms = mn == neg_inf() ? 0.f : mn;
     const float f = fast_exp2(m - ms), e = fast_exp2(s - ms);
-    l = l * f + e;
+    float sum = e;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      o[c] = fmaf(e, row < 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(p.vpages[at + c]) << 16), o[c] * f);
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    l = l * f + sum;
+    if (l != l) break;   // all is NaN from here on, whatever follows
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = finite(o[c]) ? o[c] * f : o[c];
     m = mn;
-    if (e != e) break;   // all is NaN from here on, whatever follows
+#pragma unroll 8
+    for (int x = 0; x < 32; ++x) {
+      const int row = __shfl_sync(0xffffffffu, mine, x);
+      const float w = __shfl_sync(0xffffffffu, e, x);
+      uint32_t v[D / 64] = {};
+      if (row >= 0) load_lane<D>(p.vpages + (static_cast<long long>(row) * heads + head) * D, lane, v);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o[c] = add_weighted(w * kDown, c & 1 ? bf16_hi(v[c / 2]) : bf16_lo(v[c / 2]), o[c]);
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : kUp / l;
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] *= inv;
   *lse2 = l == 0.f ? neg_inf() : m + log2f(l);
+}
+
+// A row that is not finite though the sum of its weights is, or whose values were cleaned: its channels over the keys
+// [j0, j1) as they came out, and as they have to be.
+template <int D>
+struct RowResult {
+  float o[D / 32], lse2;
+};
+template <int D>
+__device__ __forceinline__ RowResult<D> settle_row(const PagedAttendParams& p, const SequenceRows rows, int hk, long long row,
+                                                int j0, int j1, RowResult<D> r) {
+  const int lane = threadIdx.x & 31;
+  auto cache_row = [&](int j) { return rows.row_or(j, -2); };
+  FirstNonFinite<D> odd;
+  odd.look(p, p.Hk, hk, j0, j1, cache_row, lane);
+  if (odd.settle(r.o, j1)) attend_row_exact<D>(p, p.Hk, hk, row, j0, j1, cache_row, lane, r.o, &r.lse2);
+  return r;
 }
 
 // ------------------------------------------------------------------ few rows
@@ -254,6 +399,22 @@ struct KvRing {
         cp_async_16(dst + x * RP * ROW + HALF, vbase + off, kr < 0 ? 0u : 16u);
       }
     }
+  }
+  // Makes the values of step `it` finite from its key `from` on, each lane those that it brought in; true where one was not.
+  __device__ __forceinline__ bool clean_values(int it, uint8_t* smem, int from) const {
+    uint8_t* const at = smem + (ring - smem_u32(smem)) + (it % ST) * (2 * HALF) + HALF;
+    constexpr int RP = 256 / D;
+    const int mine = (threadIdx.x & 31) / (D / 8);
+    bool any = false;
+    for (int x = 0; x < KT / RP; ++x) {
+      if (x * RP + mine < from) continue;
+      uint4* const v = reinterpret_cast<uint4*>(at + x * RP * ROW);
+      if (odd_so_far(0u, *v)) {
+        *v = cleaned(*v);
+        any = true;
+      }
+    }
+    return any;
   }
   __device__ __forceinline__ uint32_t keys(int it, uint8_t* smem, int warp) const {
     return smem_u32(smem) + warp * BYTES + (it % ST) * (2 * HALF);
@@ -374,12 +535,16 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
 #pragma unroll
     for (int n = 0; n < KS; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
   }
+  const int unseen = lim_of(0);    // from here on there are keys that some row does not see
+  const int mixed = unseen < kend ? unseen - R::KT : 0x7FFFFFFF;   // ... in the steps whose first key is past this one
+  bool dirty = false;              // some of those keys' values were not finite
   for (int it = 0; it < mine; ++it) {
     issue(it + R::ST - 1);
     cp_async_wait<R::ST - 1>();
+    const int j0 = kbeg + (warp + it * R::NW) * R::KT, j = j0 + gr;
+    if (j0 > mixed) dirty = kv.clean_values(it, smem, unseen - j0) || dirty;
     __syncwarp();
     const uint32_t kt = kv.keys(it, smem, warp);
-    const int j = kbeg + (warp + it * R::NW) * R::KT + gr;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float s[4];
@@ -425,7 +590,7 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int y = 4; y < 32; y <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], y);
-  __syncthreads();
+  dirty = __syncthreads_or(dirty);
   // merge the warps' parts: [warp][row][OS] and the rows' (m, l) behind them
   float* mo = reinterpret_cast<float*>(smem);
   float* ml = mo + R::NW * ROWS * OS;
@@ -463,12 +628,19 @@ __global__ void __launch_bounds__(128) attend_rows_kernel(const __grid_constant_
 #pragma unroll
     for (int c = 0; c < CL; ++c) {
       acc[c] *= inv;
-      fine = fine && fabsf(acc[c]) < __int_as_float(0x7f800000);
+      fine = fine && finite(acc[c]);
     }
     const long long row = row_of(r);
-    if (!__all_sync(0xffffffffu, fine))
-      attend_row_exact<D>(p, p.Hk, hk, row, kbeg, min(kend, lim_of(r)), [&](int j) { return rows.row_or(j, -2); }, lane,
-                          acc, &lse2);
+    if (rl == rl && (dirty || !__all_sync(0xffffffffu, fine))) {
+      RowResult<D> x;
+#pragma unroll
+      for (int c = 0; c < CL; ++c) x.o[c] = acc[c];
+      x.lse2 = lse2;
+      x = settle_row<D>(p, rows, hk, row, kbeg, min(kend, lim_of(r)), x);
+#pragma unroll
+      for (int c = 0; c < CL; ++c) acc[c] = x.o[c];
+      lse2 = x.lse2;
+    }
     if (p.part_o) {
       const long long at = static_cast<long long>(split) * p.rows.T * p.Hq + row;
 #pragma unroll
@@ -511,15 +683,27 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float z = m == neg_inf() ? 0.f : m;
-  float l = 0.f, acc[CL] = {};
-#pragma unroll 4
-  for (int s = w; s < parts; s += NW) {
-    const float f = fast_exp2(p.part_lse[s * rows + row] - z);
-    const float* o = p.part_o + (s * rows + row) * D + lane * CL;
-    l += f;
+  float l, acc[CL];
+  auto add_up = [&](auto weigh) {
+    l = 0.f;
 #pragma unroll
-    for (int c = 0; c < CL; ++c) acc[c] = fmaf(f, o[c], acc[c]);
-  }
+    for (int c = 0; c < CL; ++c) acc[c] = 0.f;
+#pragma unroll 4
+    for (int s = w; s < parts; s += NW) {
+      const float f = fast_exp2(p.part_lse[s * rows + row] - z);
+      const float* o = p.part_o + (s * rows + row) * D + lane * CL;
+      l += f;
+#pragma unroll
+      for (int c = 0; c < CL; ++c) acc[c] = weigh(f, o[c], acc[c]);
+    }
+  };
+  add_up([](float f, float o, float sum) { return fmaf(f, o, sum); });
+  bool fine = true;
+#pragma unroll
+  for (int c = 0; c < CL; ++c) fine = fine && fabsf(acc[c]) < 0x1p126f;
+  // a part's infinity times a weight of zero, or a sum past the type's end (four warps' together)
+  if (WIDE) fine = !__syncthreads_or(!fine);
+  if (!fine) add_up([](float f, float o, float sum) { return add_weighted(f * kDown, o, sum); });
   if (WIDE) {
     if (lane == 0) sm_l[w] = l;
 #pragma unroll
@@ -533,7 +717,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
       for (int c = 0; c < CL; ++c) acc[c] += sm_a[y][lane * CL + c];
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : (fine ? 1.f : kUp) / l;
 #pragma unroll
   for (int c = 0; c < CL; c += 2)
     *reinterpret_cast<uint32_t*>(p.out + row * D + lane * CL + c) = pack_bf16(acc[c] * inv, acc[c + 1] * inv);

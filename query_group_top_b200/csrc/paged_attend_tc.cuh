@@ -8,6 +8,8 @@
 //               brings keys and values in by TMA, one box per page and 64
 //               channels (a page of 128 rows or more: per tile), through one
 //               ring of key and value tiles
+//   warp 2      goes through the values of the last tiles (mixed), which some rows
+//               see in part, between their landing and the products
 //   warps 2, 3  the producer for pages of fewer than 8 rows (GATHER), which TMA
 //               cannot lay into the swizzled tiles: every key row looked up by
 //               itself and copied in 16-byte pieces (cp.async)
@@ -46,8 +48,9 @@ struct TcCfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = 2 * TILE;
   static constexpr int OFF_BAR = OFF_RING + NST * TILE;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;      // barriers, alignment slack
-  static constexpr int THREADS = 128 + 256;               // three warpgroups, two warps of the first idle
+  static constexpr int SMEM = OFF_BAR + 288 + 1024;      // barriers, alignment slack
+  static constexpr int THREADS = 128 + 256;               // three warpgroups
+  static constexpr int MIXED = 3;                        // key tiles that some of a CTA's rows see in part
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // + t * 128, + t * D
   // registers a thread: 168 at launch, moved from the first warpgroup to the softmax ones, which hold 128 scores
   static constexpr int REGS_FEW = 72, REGS_MANY = 216;
@@ -89,6 +92,53 @@ __device__ __forceinline__ void exp2_poly(float xa, float xb, float& a, float& b
   b = __uint_as_float((__float_as_uint(nb) << 23) + __float_as_uint(rb));
 }
 
+// Rows that are not finite though the sum of their weights is, or whose values were cleaned (paged_attend.cuh), by a
+// softmax warp: a bit of `todo` each, lane x's row.  seq: sequence and tile.  What the kernel knows besides is worked out
+// again, so that its loop need not hold it.
+template <int D>
+__device__ __forceinline__ void settle_rows(const PagedAttendParams& p, const volatile int* seq, unsigned todo) {
+  constexpr int CL = D / 32;
+  const int lane = threadIdx.x & 31, b = seq[0];
+  const int hk = static_cast<int>(blockIdx.x % p.Hk), split = static_cast<int>(blockIdx.x / p.Hk % p.nsplit_many);
+  const NewSpan sp = p.rows.span(b);
+  const int chunk = chunk_of(sp, p), kbeg = split * chunk;
+  // the lane's packed row (rows behind the last have no bit), and the keys that it sees: rows further on see no fewer
+  const int pr = min(seq[1] * (2 * TcCfg<D>::BM) + static_cast<int>(threadIdx.x) - 128, sp.n * p.grp - 1), tok = pr / p.grp;
+  const long long row = (static_cast<long long>(sp.tok0) + tok) * p.Hq + hk * p.grp + (pr - tok * p.grp);
+  const int seen = min(sp.ok ? sp.len - sp.n + p.self_key + tok : 0, kbeg + chunk);
+  const SequenceRows rows(p.rows, b);
+  auto cache_row = [&](int j) { return rows.row_or(j, -2); };
+  FirstNonFinite<D> odd;
+  odd.look(p, p.Hk, hk, kbeg, __shfl_sync(0xffffffffu, seen, 31 - __clz(todo)), cache_row, lane);
+  for (; todo; todo &= todo - 1) {
+    const int x = __ffs(todo) - 1;
+    const long long rx = __shfl_sync(0xffffffffu, row, x);
+    const int lx = __shfl_sync(0xffffffffu, seen, x);
+    const long long ax = static_cast<long long>(split) * p.rows.T * p.Hq + rx;
+    float* const part = p.part_o + ax * D + lane * CL;
+    uint16_t* const out = p.out + rx * D + lane * CL;
+    float o[CL], z;
+#pragma unroll
+    for (int c = 0; c < CL; ++c) o[c] = p.part_o ? part[c] : __uint_as_float(static_cast<uint32_t>(out[c]) << 16);
+    if (odd.settle(o, lx)) {
+      attend_row_exact<D>(p, p.Hk, hk, rx, kbeg, lx, cache_row, lane, o, &z);
+      if (lane == 0) {
+        if (p.part_o)
+          p.part_lse[ax] = z;
+        else if (p.lse)
+          p.lse[rx] = z * kLn2;
+      }
+    }
+    if (p.part_o) {
+#pragma unroll
+      for (int c = 0; c < CL; ++c) part[c] = o[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < CL; c += 2) *reinterpret_cast<uint32_t*>(out + c) = pack_bf16(o[c], o[c + 1]);
+    }
+  }
+}
+
 template <int D, bool GATHER>
 __global__ void __launch_bounds__(TcCfg<D>::THREADS, 1)
 attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -107,12 +157,12 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   auto p_bar = [&](int t) { return bar0 + 8u * (B0 + 3 + t); };    // the early weights of tile t are in TMEM
   auto w_bar = [&](int t) { return bar0 + 8u * (B0 + 5 + t); };    // ... the rest of them
   auto o_bar = [&](int t) { return bar0 + 8u * (B0 + 7 + t); };    // the last product of tile t is done
-  const uint32_t tail_bar = bar0 + 8u * (B0 + 9);
-  const uint32_t done_bar = bar0 + 8u * (B0 + 10);
-  static_assert(8 * (2 * C::NST + 11) <= 224, "barriers");
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 224);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 228);
-  int* seq_s = reinterpret_cast<int*>(smem + C::OFF_BAR + 232);
+  auto land_bar = [&](int k) { return bar0 + 8u * (B0 + 9 + k); }; // the values of the k-th mixed tile have landed
+  const uint32_t done_bar = bar0 + 8u * (B0 + 9 + C::MIXED);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 240);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 244);
+  int* seq_s = reinterpret_cast<int*>(smem + C::OFF_BAR + 248);
+  volatile int* dirty_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + 256);   // some were not finite
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   grid_launch_dependents();
@@ -124,25 +174,18 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   if (warp == 0) {
     int tile = 0;
     const int b = locate_tile(p, 2 * C::BM, flat, lane, &tile);
+    // a barrier a lane, in their order above
+    constexpr int BARS = B0 + 10 + C::MIXED;
+    static_assert(BARS <= 30, "a barrier a lane, below the words at 240");
+    if (lane < BARS)
+      mbar_init(bar0 + 8u * lane, lane < C::NST ? (GATHER ? 64 : 1) : lane == B0 ? 256 : lane >= B0 + 3 && lane < B0 + 7 ? 4 : 1);
     if (lane == 0) {
       seq_s[0] = b;
       seq_s[1] = tile;
-      for (int s = 0; s < C::NST; ++s) {
-        mbar_init(full_bar(s), GATHER ? 64 : 1);
-        mbar_init(empty_bar(s), 1);
-      }
-      mbar_init(q_bar, 256);
-      for (int t = 0; t < 2; ++t) {
-        mbar_init(s_bar(t), 1);
-        mbar_init(p_bar(t), 4);
-        mbar_init(w_bar(t), 4);
-        mbar_init(o_bar(t), 1);
-      }
-      mbar_init(tail_bar, 1);
-      mbar_init(done_bar, 1);
       *abort_flag = 0;
-      fence_barrier_init();
+      *dirty_flag = 0;
     }
+    fence_barrier_init();
   }
   __syncthreads();
   const int b = seq_s[0], r0 = seq_s[1] * (2 * C::BM);
@@ -163,7 +206,13 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     kend[t] = first < total ? min(lim_of(last), kbeg + chunk) : 0;
     nk[t] = max(0, (kend[t] - kbeg + C::BN - 1) / C::BN);
   }
-  const int n = max(nk[0], nk[1]);
+  const int n = max(nk[0], nk[1]), end = max(kend[0], kend[1]);
+  // From the first key on that some row does not see, and from its tile (256 rows
+  // see keys at most 255 apart, so C::MIXED tiles), the values are gone through
+  // between landing and the products: made finite and, behind the last key that
+  // anyone sees, zeros (0 * NaN is not 0).
+  auto first_unseen = [&]() { return lim_of(r0); };
+  auto first_mixed = [&](int unseen) { return max(0, (unseen - kbeg) / C::BN); };
   if (n == 0 && split > 0) return;                          // the join reads no part a row has no keys in
 
   // the shares move inside each side's branch: ahead of it, the whole of both sides gets the smaller one
@@ -172,7 +221,6 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
   }
   if (!GATHER && warp == 0) {
     // ------------------------------------------------------------ producer
-    const int end = max(kend[0], kend[1]);
     const int page_rows = min(1 << p.rows.log2_page, C::BN);
     const int boxes = C::BN / page_rows;                    // pages (or parts of one) a tile: at most 16
     const int out_row = p.rows.num_pages << p.rows.log2_page;   // past the cache: TMA fills zeros
@@ -189,15 +237,18 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     };
     int use = 0;
     bool ok = true;
-    // the next slot of the ring, empty, its barrier told of a tile; -1: given up
-    auto slot = [&](uint32_t bar_of_tail) -> int {
+    const int mixed = first_mixed(first_unseen());
+    // the barrier of tile i's values
+    auto value_bar = [&](int i, int s) { return i < mixed ? full_bar(s) : land_bar(i - mixed); };
+    // the next slot of the ring, empty, its barrier told of a tile (of values, or of keys: i < 0); -1: given up
+    auto slot = [&](int i) -> int {
       const int s = use % C::NST, u = use / C::NST;
       if (u > 0) {
         ok = ok && mbar_wait(empty_bar(s), (u - 1) & 1, abort_flag, p.status, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) return -1;
-      if (lane == 0) mbar_arrive_expect_tx(bar_of_tail ? bar_of_tail : full_bar(s), C::TILE);
+      if (lane == 0) mbar_arrive_expect_tx(i < 0 ? full_bar(s) : value_bar(i, s), C::TILE);
       __syncwarp();
       ++use;
       return s;
@@ -213,48 +264,61 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
     }
-    bool tail_used = false;
     int next = box_row(0);
     for (int i = 0; i < n; ++i) {
       const int row = next;
       next = box_row(i + 1);
-      int s = slot(0);
+      int s = slot(-1);
       if (s < 0) break;
       load(&tm_k, s, full_bar(s), row);
-      // the last tile's rows behind the last key that anyone sees may hold
-      // anything (0 * NaN is not 0): its values are landed here, zeroed there,
-      // and only then handed on
-      const int valid = end - (kbeg + i * C::BN);
-      if (valid >= C::BN) {
-        s = slot(0);
-        if (s < 0) break;
-        load(&tm_v, s, full_bar(s), row);
-      } else {
-        s = slot(tail_bar);
-        if (s < 0) break;
-        load(&tm_v, s, tail_bar, row);
-        tail_used = true;
-        ok = mbar_wait(tail_bar, 0, abort_flag, p.status, p.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        uint8_t* at = smem + C::OFF_RING + s * C::TILE;
-        for (int x = valid * 8 + lane; x < C::BN * 8; x += 32) {
-#pragma unroll
-          for (int a = 0; a < C::ATOMS; ++a)
-            *reinterpret_cast<uint4*>(at + a * C::ATOM + x * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full_bar(s));
-        if (!ok) break;
-      }
+      s = slot(i);
+      if (s < 0) break;
+      load(&tm_v, s, value_bar(i, s), row);
     }
     // never leave the CTA with a copy still landing in its shared memory
-    if (tail_used) mbar_wait_cleanup(tail_bar, 0);
-    for (int u = max(0, use - C::NST); u < use; ++u) mbar_wait_cleanup(full_bar(u % C::NST), (u / C::NST) & 1);
+    for (int u = max(0, use - C::NST); u < use; ++u) {
+      const int s = u % C::NST;
+      if (u % 2 == 1 && u / 2 >= mixed)
+        mbar_wait_cleanup(land_bar(u / 2 - mixed), 0);
+      else
+        mbar_wait_cleanup(full_bar(s), (u / C::NST) & 1);
+    }
+  } else if (!GATHER && warp == 2) {
+    // ------------------------------------------------------------ values of the mixed tiles
+    const int unseen = first_unseen(), mixed = first_mixed(unseen);
+    for (int i = mixed; i < n; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(land_bar(i - mixed), 0, abort_flag, p.status, p.wait_ns))) break;
+      const int s = (2 * i + 1) % C::NST, j0 = kbeg + i * C::BN;
+      uint4* const at = reinterpret_cast<uint4*>(smem + C::OFF_RING + s * C::TILE);
+      // rows [from, upto) hold what some see, those behind it nothing; in 16-byte pieces, eight a row and atom
+      const int from = max(0, unseen - j0) * 8, upto = min(C::BN, end - j0) * 8;
+      for (int x = upto + lane; x < C::BN * 8; x += 32)
+#pragma unroll
+        for (int a = 0; a < C::ATOMS; ++a) at[a * (C::ATOM / 16) + x] = make_uint4(0, 0, 0, 0);
+      constexpr int STEP = 8 / C::ATOMS;                    // eight loads in flight
+      bool any = false;
+      for (int x0 = from + lane; x0 < upto; x0 += 32 * STEP) {
+        uint4 v[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) v[y] = at[y % C::ATOMS * (C::ATOM / 16) + min(x0 + y / C::ATOMS * 32, upto - 1)];
+        uint32_t odd = 0;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) odd = odd_so_far(odd, v[y]);
+        if (!odd) continue;
+        any = true;
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          at[y % C::ATOMS * (C::ATOM / 16) + min(x0 + y / C::ATOMS * 32, upto - 1)] = cleaned(v[y]);
+      }
+      if (any) *dirty_flag = 1;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full_bar(s));
+    }
   } else if (GATHER && (warp == 2 || warp == 3)) {
     // ------------------------------------------------------------ producers, row by row
     constexpr int CH = D / 8, RP = 32 / CH;                 // pieces of a row, rows that a warp's 32 pieces make
-    const int end = max(kend[0], kend[1]);
+    const int unseen = first_unseen(), mixed = first_mixed(unseen);
     const int ch = lane % CH, kw = (warp - 2) * 64;         // the lane's piece; the warp's first key of a tile
     const uint16_t* kb = p.kpages + static_cast<long long>(hk) * D + ch * 8;
     const uint16_t* vb = p.vpages + static_cast<long long>(hk) * D + ch * 8;
@@ -269,7 +333,8 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     };
     int use = 0;
     bool ok = true;
-    auto fill = [&](const uint16_t* base, int r0_, int r1_) {
+    // from: the first key of the tile whose piece is gone through (values alone)
+    auto fill = [&](const uint16_t* base, int r0_, int r1_, int from) {
       const int s = use % C::NST, u = use / C::NST;
       if (u > 0) {
         ok = mbar_wait(empty_bar(s), (u - 1) & 1, abort_flag, p.status, p.wait_ns);
@@ -286,7 +351,23 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           cp_async_16(dst + key * 128 + (((ch & 7) ^ (key & 7)) << 4), base + max(row, 0) * stride, row < 0 ? 0u : 16u);
         }
       }
-      cp_async_arrive_noinc(full_bar(s));
+      if (from < C::BN) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        bool any = false;
+        for (int key = kw + lane / CH; key < kw + 64; key += RP) {
+          if (key < from) continue;
+          uint4* const v = reinterpret_cast<uint4*>(smem + C::OFF_RING + s * C::TILE + (ch >> 3) * C::ATOM + key * 128 +
+                                                    (((ch & 7) ^ (key & 7)) << 4));
+          if (odd_so_far(0u, *v)) {
+            *v = cleaned(*v);
+            any = true;
+          }
+        }
+        if (any) *dirty_flag = 1;
+        mbar_arrive(full_bar(s));
+      } else {
+        cp_async_arrive_noinc(full_bar(s));
+      }
       ++use;
     };
     int n0 = key_row(0, 0), n1 = key_row(0, 1);
@@ -294,8 +375,8 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       const int c0 = n0, c1 = n1;
       n0 = key_row(i + 1, 0);
       n1 = key_row(i + 1, 1);
-      fill(kb, c0, c1);
-      if (ok) fill(vb, c0, c1);
+      fill(kb, c0, c1, C::BN);
+      if (ok) fill(vb, c0, c1, i < mixed ? C::BN : max(0, unseen - (kbeg + i * C::BN)));
     }
     // never leave the CTA with a copy still landing in its shared memory
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -447,7 +528,8 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const uint32_t tmem = *tmem_slot;
 
     const int pr = r0 + t * C::BM + r;                      // packed row
-    const bool row_ok = pr < total;
+    // row of q and out, -1 behind the last
+    const int qrow = pr < total ? (sp.tok0 + pr / p.grp) * p.Hq + hk * p.grp + pr % p.grp : -1;
     const int lim = lim_of(min(pr, total - 1));
     // the warp's first row sees the fewest keys (rows behind the last are zeros and go nowhere)
     const int wlim = lim_of(min(r0 + t * C::BM + (warp & 3) * 32, total - 1));
@@ -556,7 +638,8 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       const bool sees = mine > 0 && m != neg_inf();
       const float inv = sees ? 1.f / (l + dl) : 0.f;
       const float lse2 = sees ? fmaf(m, p.scale_log2, log2f(l)) : neg_inf();
-      const long long row = row_ok ? (static_cast<long long>(sp.tok0) + pr / p.grp) * p.Hq + hk * p.grp + pr % p.grp : 0;
+      const bool row_ok = qrow >= 0;
+      const long long row = max(qrow, 0);
       const long long at = static_cast<long long>(split) * p.rows.T * p.Hq + row;
       bool fine = true;
 #pragma unroll
@@ -571,7 +654,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         for (int x = 0; x < 32; ++x) {
           if (mine > 0) reg_fence(o[x]);
           f[x] = mine > 0 ? __uint_as_float(o[x]) * inv : 0.f;
-          fine = fine && fabsf(f[x]) < __int_as_float(0x7f800000);
+          fine = fine && finite(f[x]);
         }
         if (!row_ok) continue;
         if (p.part_o) {
@@ -589,27 +672,10 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         else if (p.lse)
           p.lse[row] = lse2 * kLn2;
       }
-      // rows with a value that is not finite, one by one over the keys that they see alone
+      // rows that are not finite though their sum is, or whose values were cleaned
       __syncwarp();   // (their first result, written by the row's own lane, comes before)
-      for (unsigned todo = __ballot_sync(0xffffffffu, row_ok && !fine); todo; todo &= todo - 1) {
-        const int x = __ffs(todo) - 1;
-        const long long rx = __shfl_sync(0xffffffffu, row, x);
-        const int lx = __shfl_sync(0xffffffffu, lim, x);
-        float o[D / 32], z;
-        attend_row_exact<D>(p, p.Hk, hk, rx, kbeg, min(lx, kbeg + chunk),
-                            [&](int j) { return SequenceRows(p.rows, b).row_or(j, -2); }, lane, o, &z);
-        if (p.part_o) {
-          const long long ax = static_cast<long long>(split) * p.rows.T * p.Hq + rx;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) p.part_o[ax * D + lane * (D / 32) + c] = o[c];
-          if (lane == 0) p.part_lse[ax] = z;
-        } else {
-#pragma unroll
-          for (int c = 0; c < D / 32; c += 2)
-            *reinterpret_cast<uint32_t*>(p.out + rx * D + lane * (D / 32) + c) = pack_bf16(o[c], o[c + 1]);
-          if (lane == 0 && p.lse) p.lse[rx] = z * kLn2;
-        }
-      }
+      unsigned todo = __ballot_sync(0xffffffffu, row_ok && (!fine || *dirty_flag) && l == l);
+      if (todo) settle_rows<D>(p, seq_s, todo);
     }
   }
   tc_fence_before();

@@ -119,3 +119,140 @@ def test_append_tells_of_lengths_that_do_not_fit_in_sequences_without_new_tokens
         assert same_bits(got[0], want[0]) and same_bits(got[1], want[1])
         qg.paged_attention(q, *got, c.table, lens, 4096, cu_q=c.cu)
         assert status()[0] == qg.FLAG_BADLEN
+
+
+# ------------------------------------------------------------------ values that are not finite
+NONFINITE = [  # held, new, Hq, Hk, d, page, longest
+    ([70, 9], [1, 2], 4, 2, 64, 16, None),          # few rows, one part
+    ([300], [2], 14, 1, 128, 16, None),             # 28 packed rows: matrix tiles
+    ([300], [2], 7, 1, 128, 16, None),              # 14: few rows, two tiles of them
+    ([900], [2], 2, 2, 128, 16, 1 << 20),           # few rows, many parts
+    ([0], [150], 2, 1, 64, 64, None),               # matrix tiles from nothing
+    ([500, 40], [60, 30], 4, 2, 128, 32, 1 << 20),  # ... in parts
+    ([200], [90], 3, 1, 64, 2, None),               # ... over pages that are copied row by row
+]
+
+
+def check_not_finite(out, want, bound, what):
+    assert torch.equal(torch.isnan(out), torch.isnan(want)), what
+    inf = torch.isinf(want)
+    assert torch.equal(out[inf].double(), want[inf]), what
+    whole = torch.isfinite(want)
+    ref.close(out[whole], want[whole], bound[whole], what)
+
+
+@gpu
+@pytest.mark.parametrize("case", NONFINITE, ids=str)
+def test_attention_over_values_that_are_not_finite(case):
+    """Channel by channel the definition's: an infinity or NaN that a query sees makes its channel so, whatever its
+    weight; one that it does not see leaves it alone, in its own tile too."""
+    held, new, Hq, Hk, d, page, longest = case
+    c = ref.Cache(held, new, Hk, d, page, seed=50)
+    q = normal((sum(new), Hq, d), 51)
+    t = 0
+    rng = torch.Generator().manual_seed(52)
+    for b, n in enumerate(new):
+        S = c.lens[b]
+        put = [(0, 0, math.inf), (min(3, S - 1), 1, -math.inf), (S // 2, 2, math.nan), (S // 3, 3, math.inf),
+               (S // 2, 3, -math.inf)]
+        put += [(S - 1 - i, 8 + i % 8, (math.inf, math.nan, -math.inf)[i % 3]) for i in range(n)]          # new tokens' own
+        put += [(int(torch.randint(S, (1,), generator=rng)), 20 + i, math.inf) for i in range(12)]
+        for row, ch, x in put:
+            c.v[b][row, 0, ch] = x
+            c.vpages[int(c.table[b, row // page]), row % page, 0, ch] = x
+    out, lse = attend(c, q, True, True, **({} if longest is None else {"longest": longest}))
+    assert status()[0] == 0
+    for b, n in enumerate(new):
+        lim = [held[b] + i + 1 for i in range(n)]
+        y, z, yb, zb = ref.attention(q[t:t + n], c.k[b], c.v[b], lim, d ** -0.5)
+        check_not_finite(out[t:t + n], y, yb, f"sequence {b}")
+        ref.close(lse[t:t + n], z, zb, f"lse of sequence {b}")
+        t += n
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("held,new,longest", [(100, 1, None), (3000, 1, 1 << 20), (100, 40, None), (3000, 40, 1 << 20)])
+def test_attention_over_an_infinite_value_whose_weight_rounds_to_zero(held, new, longest, d):
+    """150 below the others in the exponent: positive by definition, zero in fp32."""
+    c = ref.Cache([held], [new], 1, d, 16, seed=53)
+    q = torch.ones((new, 1, d), dtype=torch.bfloat16, device="cuda")
+    row, low = 20, -152.0 / math.sqrt(d)
+    for pages, x in ((c.kpages, low), (c.vpages, torch.where(torch.arange(d, device="cuda") == 7, math.inf, 1.0))):
+        pages[int(c.table[0, row // 16]), row % 16, 0] = x
+    c.k[0][row, 0] = low
+    c.v[0][row, 0] = 1.0
+    c.v[0][row, 0, 7] = math.inf
+    out, _ = attend(c, q, True, True, **({} if longest is None else {"longest": longest}))
+    y, _, yb, _ = ref.attention(q, c.k[0], c.v[0], [held + i + 1 for i in range(new)], d ** -0.5)
+    check_not_finite(out, y, yb, "dense")
+    if new == 1:
+        idx = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 1, 1, 64)
+        out = qg.sparse_attention_paged(q.view(1, 1, 1, d), c.kpages, c.vpages, c.table, c.seqlens, idx)
+        y, _, yb, _ = ref.attention(q, c.k[0][:64], c.v[0][:64], [64], d ** -0.5)
+        check_not_finite(out[0], y, yb, "index rows")
+
+
+@gpu
+@pytest.mark.parametrize("case", NONFINITE, ids=str)
+def test_attention_over_values_near_the_types_end(case):
+    """Every value of a channel 3e38 (another's -3e38, a third's in turn): a mean of them is finite, a sum is not."""
+    held, new, Hq, Hk, d, page, longest = case
+    c = ref.Cache(held, new, Hk, d, page, seed=56)
+    q = normal((sum(new), Hq, d), 57)
+    for b, n in enumerate(new):
+        for row in range(c.lens[b]):
+            big = torch.tensor([3e38, -3e38, 3e38 if row % 2 else -3e38], device="cuda").to(torch.bfloat16)
+            c.v[b][row, 0, 4:7] = big
+            c.vpages[int(c.table[b, row // page]), row % page, 0, 4:7] = big
+    out, _ = attend(c, q, True, True, **({} if longest is None else {"longest": longest}))
+    assert status()[0] == 0
+    t = 0
+    for b, n in enumerate(new):
+        y, _, yb, _ = ref.attention(q[t:t + n], c.k[b], c.v[b], [held[b] + i + 1 for i in range(n)], d ** -0.5)
+        ref.close(out[t:t + n], y, yb, f"sequence {b}")
+        t += n
+    if len(held) == 1 and new[0] == 2 and Hq == Hk:
+        idx = torch.arange(held[0], dtype=torch.int32, device="cuda").expand(1, 2, Hq, held[0]).contiguous()
+        out = qg.sparse_attention_paged(q.view(1, 2, Hq, d), c.kpages, c.vpages, c.table, c.seqlens, idx)
+        y, _, yb, _ = ref.attention(q, c.k[0][:held[0]], c.v[0][:held[0]], [held[0]] * 2, d ** -0.5)
+        ref.close(out[0], y, yb, "index rows")
+
+
+def microseconds(f):
+    f()
+    torch.cuda.synchronize()
+    best = math.inf
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, 1000 * a.elapsed_time(b))
+    return best
+
+
+@gpu
+@pytest.mark.parametrize("what", ["prefill", "chunk", "decode", "index rows"])
+def test_a_value_that_is_not_finite_costs_a_few_calls_not_hundreds(what):
+    """An overflowed value at a sequence's start stands in every later row.  The bound of 20 calls' time is far from
+    both sides: 2 to 4 with the values looked at once, 60 to 900 with every row walked key by key."""
+    held, new, Hq, Hk, d, page = {"prefill": ([0], [3000], 8, 8, 64, 64), "chunk": ([6000], [300], 16, 4, 128, 64),
+                                  "decode": ([8000] * 16, [1] * 16, 32, 8, 128, 16),
+                                  "index rows": ([2500] * 16, [2] * 16, 16, 16, 128, 16)}[what]
+    c = ref.Cache(held, new, Hk, d, page, seed=54)
+    q = normal((sum(new), Hq, d), 55)
+    if what == "index rows":
+        idx = torch.arange(2048, dtype=torch.int32, device="cuda").expand(16, 2, 16, 2048).contiguous()
+        call = lambda: qg.sparse_attention_paged(q.view(16, 2, 16, 128), c.kpages, c.vpages, c.table, c.seqlens, idx)  # noqa: E731
+    else:
+        call = lambda: qg.paged_attention(q, c.kpages, c.vpages, c.table, c.seqlens, c.longest, cu_q=c.cu)  # noqa: E731
+    plain = microseconds(call)
+    for row in (0, max(new) - 1):                    # seen by all, or by some after it
+        for b in range(len(held)):
+            c.vpages[int(c.table[b, row // page]), row % page, :, 5 + row % 7] = (math.inf, math.nan)[row % 2]
+        assert not bool(torch.isfinite(call()).all())
+        took = microseconds(call)
+        print(f"{what}: {plain:.0f} us, {took:.0f} with row {row} not finite")
+        assert took < 20 * plain, (plain, took)
