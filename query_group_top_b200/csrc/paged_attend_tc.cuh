@@ -287,7 +287,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // ------------------------------------------------------------ values of the mixed tiles
     const int unseen = first_unseen(), mixed = first_mixed(unseen);
     for (int i = mixed; i < n; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(land_bar(i - mixed), 0, abort_flag, p.status, p.wait_ns))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait<true>(land_bar(i - mixed), 0, abort_flag, p.status, p.wait_ns))) break;
       const int s = (2 * i + 1) % C::NST, j0 = kbeg + i * C::BN;
       uint4* const at = reinterpret_cast<uint4*>(smem + C::OFF_RING + s * C::TILE);
       // rows [from, upto) hold what some see, those behind it nothing; in 16-byte pieces, eight a row and atom
@@ -399,7 +399,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
       const uint64_t qd = sw128_kmajor_desc(sbase + C::OFF_Q), kd = sw128_kmajor_desc(ring);
       const uint64_t vd = sw128_nmajor_desc(ring, C::ATOM);
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait<GATHER>(bar, parity, abort_flag, p.status, p.wait_ns)) != 0;
       };
       // slot and phase of the ring's next tile (key tile i, then value tile i, ...)
       int slot = 0;

@@ -56,6 +56,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether the phase is complete, now: mbar_try_wait may suspend the thread for a
+// time of the hardware's choice first.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // As mbar_try_wait, but a thread whose phase is not complete yet is suspended
 // in hardware (it takes no issue slots) until the phase completes or about
 // `hint_ns` nanoseconds have passed.
@@ -80,13 +94,19 @@ constexpr uint32_t kSuspendNs = 20000;
 // Returns false (and sets *abort, raising kStTimeout) after limit_ns, or
 // returns false at once when another role has already set *abort.  Between
 // polls the warp is suspended on the barrier itself (mbar_try_wait_suspend),
-// so waiting warps leave the issue slots to the warps they wait for.
+// so waiting warps leave the issue slots to the warps they wait for.  PROMPT:
+// under a limit shorter than a suspension nothing is suspended, for kernels whose
+// waits are all shorter than the hardware's least (a role of such a kernel is enough:
+// the others see that it gave up).
+template <bool PROMPT = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
                                           unsigned long long limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  const bool prompt = PROMPT && limit_ns < kSuspendNs;
+  if (prompt ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_timer_ns();
   while (true) {
-    if (mbar_try_wait_suspend(bar, parity, min(kSuspendNs, static_cast<uint32_t>(min(limit_ns, 0xFFFFFFFFull)))))
+    if (prompt ? mbar_test_wait(bar, parity)
+               : mbar_try_wait_suspend(bar, parity, min(kSuspendNs, static_cast<uint32_t>(min(limit_ns, 0xFFFFFFFFull)))))
       return true;
     if (*abort) return false;
     if (global_timer_ns() - t0 > limit_ns) {

@@ -35,6 +35,16 @@ def test_index_rows_longer_than_their_places_count_are_refused():
         assert b"top_k" in lib.pivot_last_error()
 
 
+def test_no_workspace_where_the_rows_fill_the_device():
+    """Parts of the key axis are for few rows: a prefill whose row tiles are several rounds of the device's has none."""
+    from query_group_top_b200 import build
+    build.build()
+    size = qg.load_library().pivot_paged_attention_workspace_size
+    assert size(8192, 1, 16, 16, 128, 8192) == 0
+    assert size(2048, 64, 32, 8, 128, 2048) == 0
+    assert size(64, 1, 16, 16, 128, 8192) > 0
+
+
 # ------------------------------------------------------------------ sequences that do not fit
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
@@ -256,3 +266,33 @@ def test_a_value_that_is_not_finite_costs_a_few_calls_not_hundreds(what):
         took = microseconds(call)
         print(f"{what}: {plain:.0f} us, {took:.0f} with row {row} not finite")
         assert took < 20 * plain, (plain, took)
+
+
+# ------------------------------------------------------------------ waits that run out
+@gpu
+@pytest.mark.parametrize("page", [2, 16])        # rows copied one by one, and by TMA
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [1, 90])           # parts of two key tiles; rings that are filled more than once
+def test_attention_gives_up_under_a_limit_of_a_nanosecond(B, d, page):
+    """Under a limit that no wait for memory or for the products keeps, a call gives up and says so, and leaves the device
+    as it was: the next call is exact."""
+    c = ref.Cache([9000 if B == 1 else 1500] * B, [64] * B, 2, d, page, seed=58)
+    q = normal((64 * B, 4, d), 59)
+    want, lse = attend(c, q, True, True)
+    assert status()[0] == 0
+    lib = qg.load_library()
+    told = 0
+    try:
+        lib.pivot_set_wait_limit(1)
+        for _ in range(20):
+            attend(c, q, True, True)
+            flags, message = status()
+            assert flags in (0, qg.FLAG_TIMEOUT) and ("timed out" in message) == (flags != 0)
+            told += flags != 0
+    finally:
+        lib.pivot_set_wait_limit(0)
+    print(f"{told} of 20 calls gave up")
+    assert told > 0
+    again, lse2 = attend(c, q, True, True)
+    assert status()[0] == 0
+    assert same_bits(again, want) and same_bits(lse, lse2)
