@@ -343,6 +343,9 @@ def _load_step():
     except ImportError as e:
         raise PivotError(f"the binding of the serving step does not load ({e}): build it with "
                          "`python -m query_group_top_b200.build`") from e
+    if getattr(m, "built_for", None) != torch.__version__:
+        raise PivotError(f"the binding of the serving step was not built for this torch ({torch.__version__}): "
+                         "build it with `python -m query_group_top_b200.build`")
     m.bind(PivotError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
         "pivot_last_error", "pivot_qk_rope", "pivot_paged_append", "pivot_paged_attention_workspace_size",
         "pivot_paged_attention", "pivot_sparse_attention_paged")))

@@ -491,4 +491,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, methods, null
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__step() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__step() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch whose C++ classes this calls: another version may lay them out otherwise
+  if (m && PyModule_AddStringConstant(m, "built_for", PIVOT_TORCH) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

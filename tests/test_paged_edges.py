@@ -35,6 +35,23 @@ def test_index_rows_longer_than_their_places_count_are_refused():
         assert b"top_k" in lib.pivot_last_error()
 
 
+def test_a_binding_built_for_another_torch_is_told_and_built_anew(monkeypatch, tmp_path):
+    """The compiled half of the binding calls one torch's C++ classes: another torch's is neither loaded nor left."""
+    from query_group_top_b200 import build
+    build.build()
+    assert not build.stale(build.BINDING) and build.built_for() == torch.__version__
+    assert qg._load_step().built_for == torch.__version__
+    monkeypatch.setattr(build, "torch_version", lambda: "9.9.9")
+    assert build.stale(build.BINDING) and not build.stale(build.LIB)
+    monkeypatch.undo()
+    monkeypatch.setattr(build, "BUILT_FOR", str(tmp_path / "none.txt"))
+    assert build.stale(build.BINDING)                      # built when nobody wrote it down
+    monkeypatch.undo()
+    monkeypatch.setattr(qg.torch, "__version__", "9.9.9")
+    with pytest.raises(qg.PivotError, match="not built for this torch"):
+        qg._load_step()
+
+
 def test_no_workspace_where_the_rows_fill_the_device():
     """Parts of the key axis are for few rows: a prefill whose row tiles are several rounds of the device's has none."""
     from query_group_top_b200 import build
