@@ -1,5 +1,7 @@
 """Builds in-tree the CUDA library ``libpivot.so`` for sm_100a with nvcc, and the compiled half of the Python binding
 (``_step``, host code alone, against the torch that is installed) with the host compiler.
+
+    python -m query_group_top_b200.build [-v] [--library]      # --library: libpivot.so alone, which needs nvcc and no torch
 """
 import os
 import subprocess
@@ -73,16 +75,17 @@ def build_binding(verbose: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
+def build(force: bool = False, verbose: bool = False, binding: bool = True) -> str:
+    """The library, and with `binding` the compiled half of the binding, where they are missing or stale."""
     if force or stale(LIB):
         nvcc = os.environ.get("NVCC", "nvcc")
         _run([nvcc, *(["-Xptxas=-v"] if verbose else []), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"),
               os.path.join(SRC, "pivot.cu")], LIB, verbose)
-    if force or stale(BINDING):
+    if binding and (force or stale(BINDING)):
         build_binding(verbose)
     return LIB
 
 
 if __name__ == "__main__":
-    build(force=True, verbose="-v" in sys.argv)
+    build(force=True, verbose="-v" in sys.argv, binding="--library" not in sys.argv)
     print(LIB)

@@ -52,6 +52,18 @@ def test_a_binding_built_for_another_torch_is_told_and_built_anew(monkeypatch, t
         qg._load_step()
 
 
+def test_the_library_is_built_without_the_binding(monkeypatch):
+    """A user of the C library alone needs neither torch nor Python's headers."""
+    from query_group_top_b200 import build
+
+    def no(*_):
+        raise AssertionError("the binding was asked for")
+
+    monkeypatch.setattr(build, "build_binding", no)
+    monkeypatch.setattr(build, "torch_version", no)
+    assert build.build(binding=False) == build.LIB
+
+
 def test_no_workspace_where_the_rows_fill_the_device():
     """Parts of the key axis are for few rows: a prefill whose row tiles are several rounds of the device's has none."""
     from query_group_top_b200 import build
