@@ -208,7 +208,8 @@ int pivot_decode_index_paged(const void* q, const void* kpages, const int32_t* b
  *    given) is skipped; a row whose page is not in [0, num_pages) is not written,
  *    and read as zeros; both are reported by pivot_sync_status() as
  *    PIVOT_ERR_INVALID_ARG.
- *  - d is 64 or 128.  fp32 arithmetic; each result is rounded once.
+ *  - d is 64 or 128.  fp32 arithmetic; each result is rounded once.  (One more
+ *    rounding in pivot_paged_attention: told there.)
  */
 
 /* Type of a call's inputs, and how a rotation pairs the first rot_dim channels:
@@ -287,8 +288,15 @@ typedef struct {
  * NULL.  options NULL:
  * scale d^-1/2, include_self.  max_seqlen: an upper bound on seqlens[b]; a
  * longer sequence is skipped.  With cu_q, g is an upper bound on a sequence's new
- * tokens, for the choice of kernels alone, or 0.  Keys and values that a query does not see may
- * hold anything.  workspace as in the _ws variants; the size may be 0.
+ * tokens, for the choice of kernels alone, or 0.  Keys and values that a query
+ * does not see may hold anything; of those that it sees, an infinite or NaN value
+ * makes its channel so, however small its weight.  workspace as in the _ws
+ * variants; the size may be 0.
+ * Scores, the softmax's sums and the results' are fp32.  Each weight is rounded to
+ * bf16 for its product with the values (the matrix instructions' operand type), and
+ * out to bf16: an error of at most 2^-8 (sum_j p_j |v_j| + |out|) beside fp32's, p
+ * being the softmax; as the weights' roundings differ, in truth about
+ * 2^-8 (sqrt(sum_j p_j^2 v_j^2) + |out|).  out_lse has none of it.
  */
 size_t pivot_paged_attention_workspace_size(int T, int B, int Hq, int Hk, int d, int max_seqlen);
 int pivot_paged_attention(const void* q, const void* kpages, const void* vpages, const int32_t* block_table,

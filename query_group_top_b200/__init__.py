@@ -450,7 +450,8 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
     include_self=False, those before it (the indexer's keys); a query that sees none gets zeros and lse -inf.
     max_seqlen bounds seqlens; max_q (with cu_q, optional) bounds a sequence's new tokens, which spares a batch of
     single tokens the launch for longer ones.  scale: d ** -0.5 by default.  out_lse: float32 [..., Hq], the log of each
-    row's sum.  Returns bf16 with q's shape."""
+    row's sum.  Returns bf16 with q's shape.  fp32 scores and sums; the weights are rounded to bf16 for their product
+    with the values."""
     step = _calls or _load_step()
     if stream is None:
         return step.paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q, scale, include_self, out,
