@@ -160,6 +160,74 @@ def test_append_tells_of_lengths_that_do_not_fit_in_sequences_without_new_tokens
         assert status()[0] == qg.FLAG_BADLEN
 
 
+# ------------------------------------------------------------------ packed rows and lengths of every path
+SIXTEEN = [  # held, new, Hq, Hk, d, page, itself, ragged, longest: 9 to 16 packed rows a sequence
+    ([300, 17, 0], [1] * 3, 16, 1, 128, 16, True, False, None),
+    ([200], [3], 12, 3, 128, 32, True, False, None),              # 12 rows
+    ([90, 500], [4, 4], 8, 2, 128, 8, False, False, None),
+    ([5000, 3], [1, 1], 32, 2, 128, 64, True, False, 1 << 20),    # many parts
+    ([1500] * 30, [2] * 30, 10, 2, 128, 16, True, False, None),   # 10 rows, two or more a scheduler
+    ([40, 700, 0, 9], [4, 1, 3, 2], 8, 2, 128, 1, True, True, None),
+    ([4000, 60], [3, 3], 5, 1, 64, 16, True, False, None),        # 15 rows of 64 channels
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", SIXTEEN, ids=str)
+def test_attention_of_nine_to_sixteen_packed_rows(case):
+    held, new, Hq, Hk, d, page, itself, ragged, longest = case
+    c = ref.Cache(held, new, Hk, d, page, seed=60)
+    q = normal((sum(new), Hq, d), 61)
+    kw = {} if longest is None else {"longest": longest}
+    out, lse = attend(c, q, itself, ragged, **kw)
+    assert status()[0] == 0
+    check_attention(c, q, out, lse, itself, d ** -0.5)
+    again, lse2 = attend(c, q, itself, ragged, **kw)
+    assert same_bits(out, again) and same_bits(lse, lse2)
+
+
+LONG = [  # held, new, Hq, Hk, d, page
+    ([0], [4096], 16, 16, 128, 128),        # 256 row tiles: more than the device takes at a time
+    ([40000], [300], 8, 2, 64, 64),         # a chunk behind a long context, in parts
+    ([60000], [2], 16, 1, 128, 16),         # 32 packed rows: matrix tiles in many parts
+    ([60000, 20000], [1, 1], 32, 2, 128, 16),   # 16 packed rows
+    ([100000], [1], 4, 4, 64, 4),
+    ([30000], [40], 4, 1, 128, 2),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_attention_over_long_contexts_within_a_narrow_bound(case):
+    """Where thousands of keys share the weight, the roundings' worst case is a tenth of a typical output and more.  They
+    are independent: a weight's is at most HALF of it, anywhere between, so its deviation at most HALF / sqrt(3), and their
+    sum's HALF / sqrt(3) sqrt(sum p^2 v^2); 7 of those (one value in 10^11) are allowed, HALF of the output twice (its own
+    rounding, and the sum's correction by the heaviest weights' roundings), and fp32's part as in paged_ref."""
+    held, new, Hq, Hk, d, page = case
+    c = ref.Cache(held, new, Hk, d, page, seed=62)
+    q = normal((sum(new), Hq, d), 63)
+    out, lse = attend(c, q, True, True)
+    assert status()[0] == 0
+    t = 0
+    for b, n in enumerate(new):
+        for h in sorted({0, Hq // 2, Hq - 1}):
+            k, v = c.k[b][:, h // (Hq // Hk)].double(), c.v[b][:, h // (Hq // Hk)].double()
+            x = q[t:t + n, h].double() @ k.T * d ** -0.5
+            ds = float((q[t:t + n, h].double().abs() @ k.abs().T).max()) * d ** -0.5 * (d + 4) * ref.FP32
+            x = x.masked_fill(torch.arange(c.lens[b], device="cuda") > torch.arange(held[b], held[b] + n, device="cuda")[:, None],
+                              -math.inf)
+            z = torch.logsumexp(x, 1)
+            p = torch.exp(x - z[:, None])
+            y, far, dev = p @ v, p @ v.abs(), (p * p @ (v * v)).sqrt()
+            soft = 2 * ds + 2.0 ** -20 + (math.sqrt(c.lens[b]) + 16) * ref.FP32
+            bound = ref.HALF * (2 * y.abs() + 7 / math.sqrt(3) * dev) + soft * far
+            ref.close(out[t:t + n, h], y, bound, f"head {h} of sequence {b}")
+            ref.close(lse[t:t + n, h], z, ds + 2.0 ** -20 + 4 * ref.FP32 * (z.abs() + x.amax(1).abs()), "lse")
+            if held[b]:
+                assert float(bound.mean()) < 0.05 * float(y.square().mean().sqrt())       # narrow indeed
+        t += n
+
+
 # ------------------------------------------------------------------ values that are not finite
 NONFINITE = [  # held, new, Hq, Hk, d, page, longest
     ([70, 9], [1, 2], 4, 2, 64, 16, None),          # few rows, one part
