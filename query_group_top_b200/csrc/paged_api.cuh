@@ -167,11 +167,13 @@ AttendPlan plan_attend(int T, int B, int Hq, int Hk, int d, int max_seqlen, int 
     a.nsplit = best_parts(units(256), sms, max_seqlen,
                           PartCost{(d == 128 ? 1400. : 1100.) / 128, 6000, 4000, part_time}, most);
   } else {
-    // an SM's share of the memory's rate, among its CTAs; some 3 us before and after
+    // a key's and its value's bytes at an SM's share of the memory's rate (41 bytes a ns of 6.1 TB/s), among its CTAs;
+    // some 3 us before and after
+    constexpr double kSmBytesPerNs = 41;
     a.rows = rows <= 8ll * B ? 8 : 16;
     const int per_sm = d == 128 ? KvRing<128>::PER_SM : KvRing<64>::PER_SM;
     a.nsplit = best_parts(units(a.rows), static_cast<long long>(per_sm) * sms, max_seqlen,
-                          PartCost{4. * d / 41. * per_sm, 3300, 4500, part_time}, most);
+                          PartCost{4. * d / kSmBytesPerNs * per_sm, 3300, 4500, part_time}, most);
   }
   // the matrix tiles' launch for long chunks among single tokens, which may find
   // none: two parts at most, so that it is over soon

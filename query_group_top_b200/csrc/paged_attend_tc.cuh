@@ -71,7 +71,8 @@ constexpr int kEarly = 3;      // quarters of a weight tile that are handed on a
 // 2^x of two values in fp32 by arithmetic alone (no special-function unit):
 // x = n + f with n whole and |f| <= 1/2, 2^f by its minimax polynomial of
 // degree 5 (fitted here by the Remez exchange; relative error 7.5e-8, with the
-// fp32 roundings below 2.2e-7), and n added to the exponent.  x below -127
+// coefficients rounded to fp32 1.6e-7, with the arithmetic's roundings below
+// 2.2e-7), and n added to the exponent.  x below -127
 // gives 0 (a subnormal), x must not be NaN.
 __device__ __forceinline__ void exp2_poly(float xa, float xb, float& a, float& b) {
   const float kMagic = 12582912.f;   // 1.5 2^23: adding it rounds to a whole number in the low bits
@@ -457,15 +458,13 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
           ok = ok && wait(p_bar(t), i & 1);
           if (!ok) break;
           tc_fence_after();
-          if (kEarly < 4) {
-            if (elect_one()) products(t, vs, 0, 2 * kEarly, i == 0);
-            __syncwarp();
-            ok = wait(w_bar(t), i & 1);
-            if (!ok) break;
-            tc_fence_after();
-          }
+          if (elect_one()) products(t, vs, 0, 2 * kEarly, i == 0);
+          __syncwarp();
+          ok = wait(w_bar(t), i & 1);
+          if (!ok) break;
+          tc_fence_after();
           if (elect_one()) {
-            products(t, vs, kEarly < 4 ? 2 * kEarly : 0, 8, i == 0);
+            products(t, vs, 2 * kEarly, 8, i == 0);
             if (i + 1 < nt)
               scores(t, ks);
             else
@@ -494,31 +493,28 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // both query tiles into shared memory in the swizzled layout: a thread takes
     // one 16-byte piece of every RS-th row (rows behind the last repeat it: they
     // go nowhere), all of its loads in flight
-    constexpr int CH = D / 8, RS = 256 / CH, STEP = CH;
+    constexpr int CH = D / 8, RS = 256 / CH;
     {
       const int ch = tid % CH, row0 = tid / CH;
       int tok = (r0 + row0) / p.grp, rem = (r0 + row0) % p.grp;   // of the packed row at hand
       const int dtok = RS / p.grp, drem = RS % p.grp;
       const int ltok = (total - 1) / p.grp, lrem = p.grp - 1;      // of the last one
       const uint16_t* qb = p.q + (static_cast<long long>(sp.tok0) * p.Hq + hk * p.grp) * D + ch * 8;
+      uint4 v[CH];
 #pragma unroll
-      for (int x0 = 0; x0 < CH; x0 += STEP) {
-        uint4 v[STEP];
+      for (int y = 0; y < CH; ++y) {
+        const bool in = tok <= ltok;
+        v[y] = __ldg(reinterpret_cast<const uint4*>(
+            qb + (static_cast<long long>(in ? tok : ltok) * p.Hq + (in ? rem : lrem)) * D));
+        tok += dtok;
+        rem += drem;
+        if (rem >= p.grp) rem -= p.grp, ++tok;
+      }
 #pragma unroll
-        for (int y = 0; y < STEP; ++y) {
-          const bool in = tok <= ltok;
-          v[y] = __ldg(reinterpret_cast<const uint4*>(
-              qb + (static_cast<long long>(in ? tok : ltok) * p.Hq + (in ? rem : lrem)) * D));
-          tok += dtok;
-          rem += drem;
-          if (rem >= p.grp) rem -= p.grp, ++tok;
-        }
-#pragma unroll
-        for (int y = 0; y < STEP; ++y) {
-          const int row = row0 + RS * (x0 + y);
-          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (ch >> 3) * C::ATOM + (row & 127) * 128 +
-                                    (((ch & 7) ^ (row & 7)) << 4)) = v[y];
-        }
+      for (int y = 0; y < CH; ++y) {
+        const int row = row0 + RS * y;
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (row >> 7) * C::TILE + (ch >> 3) * C::ATOM + (row & 127) * 128 +
+                                  (((ch & 7) ^ (row & 7)) << 4)) = v[y];
       }
     }
     fence_proxy_async_smem();
@@ -531,7 +527,7 @@ attend_tiles_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     // row of q and out, -1 behind the last
     const int qrow = pr < total ? (sp.tok0 + pr / p.grp) * p.Hq + hk * p.grp + pr % p.grp : -1;
     const int lim = lim_of(min(pr, total - 1));
-    // the warp's first row sees the fewest keys (rows behind the last are zeros and go nowhere)
+    // the warp's first row sees the fewest keys (rows behind the last repeat it and go nowhere)
     const int wlim = lim_of(min(r0 + t * C::BM + (warp & 3) * 32, total - 1));
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + C::S_COL + t * C::BN;
