@@ -7,8 +7,8 @@
 // the arithmetic.  The index of a step is read two steps before its keys and the
 // page one step before, so neither of the two dependent loads is waited for.
 // What bounds it is the chain of a step in its warp (rows, product, softmax,
-// product), three warps a scheduler: DRAM is at 50 %, the issue slots at 29.  32
-// sequences, steps of two, 16 heads of 128, 2048 indices take 154 to 163 us.  Merging the
+// product), three warps a scheduler: DRAM is at 54 %, the issue slots at 26.  32
+// sequences, steps of two, 16 heads of 128, 2048 indices take 155 to 162 us.  Merging the
 // rows of two members in a CTA, so that common keys are gathered once (0.68 GB for
 // 1.07), was built and took 173 to 182.
 //

@@ -21,7 +21,7 @@
 // stay with their token, whose cosines they hold in registers, and walk its
 // heads, so that the next row's address is one addition away and its loads run
 // ahead of the arithmetic.  Blocks of 128 threads, seven an SM: 8192 tokens of
-// 32 heads of 128, normed and turned, take 30 us, a plain copy of the same bytes
+// 32 heads of 128, normed and turned, take 29 us, a plain copy of the same bytes
 // 25; 27 of them are the kernel without norm and rotation.  32768 tokens of 40
 // heads: 123 us, the copy 113.
 #pragma once
