@@ -445,7 +445,7 @@ def paged_attention(q, kpages, vpages, block_table, seqlens, max_seqlen, cu_q=No
     """Dense causal attention of new tokens over the paged cache that holds their keys and values already.
 
     q: bf16 [B, g, Hq, d] (a decode step), or [T, Hq, d] with cu_q int32 [B + 1] (chunks of any lengths; rows of
-    tokens behind cu_q[B] are left as they were); Hq a multiple of the cache's heads, query head h reads key head
+    tokens behind cu_q[B] are left as they were, so without `out` they hold nothing of meaning); Hq a multiple of the cache's heads, query head h reads key head
     h // (Hq // Hk).  Token i of n_b sits at position seqlens[b] - n_b + i and sees the keys up to its own, or, with
     include_self=False, those before it (the indexer's keys); a query that sees none gets zeros and lse -inf.
     max_seqlen bounds seqlens; max_q (with cu_q, optional) bounds a sequence's new tokens, which spares a batch of

@@ -237,6 +237,8 @@ NONFINITE = [  # held, new, Hq, Hk, d, page, longest
     ([0], [150], 2, 1, 64, 64, None),               # matrix tiles from nothing
     ([500, 40], [60, 30], 4, 2, 128, 32, 1 << 20),  # ... in parts
     ([200], [90], 3, 1, 64, 2, None),               # ... over pages that are copied row by row
+    ([200], [90], 3, 1, 128, 4, None),
+    ([30] * 60 + [300], [1] * 60 + [90], 4, 1, 64, 16, None),   # a chunk among single tokens: both kernels
 ]
 
 
